@@ -519,3 +519,94 @@ def conv_finish_prepare(z, block_size, taps, group, dyn_out, base, W_proj, base_
                                            _p(dyn), _p(ws), _nbytes(ws), _stream(stream, dev))
     _check("dflash2_conv_finish_prepare", rc)
     return h, y, dyn
+
+
+_DTYPES = {torch.bfloat16: DF2_DTYPE_BF16, torch.float32: DF2_DTYPE_F32}
+
+
+def _rows(t, name, shape=None, dev=None):
+    """A bf16 or fp32 matrix whose rows are dense (their distance may exceed their length):
+    (its DF2_DTYPE_*, the distance in elements)."""
+    if not isinstance(t, torch.Tensor) or not _on_device(t):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be {'a matrix' if shape is None else list(shape)}, got {list(t.shape)}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else max(cols, 1)
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name} must have dense rows")
+    return dt, ld
+
+
+def _scratch(nbytes, workspace, dev, stream):
+    """The caller's workspace, or one of this call's own, which the allocator keeps from
+    other uses until the kernels of `stream` have read it."""
+    ws = _workspace(nbytes, workspace, dev)
+    if workspace is None and ws is not None and stream is not None:
+        ws.record_stream(stream)
+    return ws
+
+
+def embedding(table, ids, *, scale=1.0, dtype=None, dev_status=None, out=None, stream=None):
+    """scale * table[ids], [*ids.shape, D] in `dtype` (default: the table's).  Rows of negative
+    ids are zeros; an id >= V sets the status word and gives NaN.  table and out ([N, D])
+    may have rows further apart than their length."""
+    dt, ld = _rows(table, "table")
+    _need(ids, "ids", torch.int32)
+    V, D = table.shape
+    N = ids.numel()
+    dev = _device(table, ids=ids)
+    if out is None:
+        out = torch.empty((*ids.shape, D), dtype=table.dtype if dtype is None else dtype, device=dev)
+        odt, old = _DTYPES.get(out.dtype), D
+        if odt is None:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {out.dtype}")
+    else:
+        odt, old = _rows(out, "out", (N, D), dev)
+        if dtype is not None and dtype != out.dtype:
+            raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    _status(dev_status, dev)
+    rc = lib().dflash2_embedding(_p(table), dt, V, D, ld, _p(ids), N, float(scale), _p(out), odt, old,
+                                 _p(dev_status), _stream(stream, dev))
+    _check("dflash2_embedding", rc)
+    return out
+
+
+def embedding_grad_workspace_size(N, V, D) -> int:
+    return int(lib().dflash2_embedding_grad_workspace_size(N, V, D))
+
+
+def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=False, workspace=None,
+                   dev_status=None, out=None, stream=None):
+    """The gradient [V, D] of embedding()'s table: scale * the sum of dout's rows of each
+    token, in fp32, the same bits every time.  accumulate adds to `out`; otherwise every
+    row is written.  dout is [N, D], or [*ids.shape, D] where contiguous."""
+    _need(ids, "ids", torch.int32)
+    N = ids.numel()
+    if isinstance(dout, torch.Tensor) and dout.dim() != 2 and dout.dim() == ids.dim() + 1 and dout.is_contiguous():
+        dout = dout.view(N, dout.shape[-1])
+    dt, ld = _rows(dout, "dout")
+    D = dout.shape[1]
+    if dout.shape[0] != N:
+        raise ValueError(f"dout must have a row an id ({N}), got {dout.shape[0]}")
+    V = int(V)
+    dev = _device(dout, ids=ids)
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to out: out must be given")
+        out = torch.empty((V, D), dtype=dtype, device=dev)
+    odt, old = _rows(out, "out", (V, D), dev)
+    _status(dev_status, dev)
+    ws = _scratch(embedding_grad_workspace_size(N, V, D), workspace, dev, stream)
+    rc = lib().dflash2_embedding_grad(_p(dout), dt, ld, _p(ids), N, V, D, float(scale), int(bool(accumulate)),
+                                      _p(out), odt, old, _p(ws), _nbytes(ws), _p(dev_status), _stream(stream, dev))
+    _check("dflash2_embedding_grad", rc)
+    return out
+
+
+from .optim import AdamW  # noqa: E402  (needs the checks above)

@@ -11,7 +11,15 @@ import threading
 
 from .build import INCLUDE, LIB
 
+_f64 = ct.c_double
 _i64, _i32, _int, _vp, _sz, _f32 = ct.c_int64, ct.c_int32, ct.c_int, ct.c_void_p, ct.c_size_t, ct.c_float
+
+class AdamWTensor(ct.Structure):
+    """dflash2_adamw_tensor."""
+    _fields_ = [("param", _vp), ("master", _vp), ("grad", _vp), ("exp_avg", _vp), ("exp_avg_2", _vp),
+                ("exp_avg_scale", _vp), ("exp_avg_2_scale", _vp), ("n", _i64), ("param_dtype", _int),
+                ("grad_dtype", _int), ("lr", _f64), ("weight_decay", _f64)]
+
 
 SIGNATURES = {
     "dflash2_status_string": (ct.c_char_p, [_int]),
@@ -45,6 +53,11 @@ SIGNATURES = {
     "dflash2_conv_finish_prepare_workspace_size": (_sz, [_i64, _int, _int, _int, _int]),
     "dflash2_conv_finish_prepare": (_int, [_vp, _int, _i64, _int, _int, _int, _int, _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dflash2_embedding": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _f32, _vp, _int, _i64, _vp, _vp]),
+    "dflash2_embedding_grad_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "dflash2_embedding_grad": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _f32, _int, _vp, _int, _i64, _vp, _sz,
+                                      _vp, _vp]),
+    "dflash2_adamw": (_int, [_vp, _int, _int, _f64, _f64, _f64, _i64, _vp, _vp]),
 }
 
 _lock = threading.Lock()

@@ -37,6 +37,13 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rn(float f) {
     return uint16_t(u >> 16);
 }
 
+// Two fp32 to a word of two bf16 (lo in the low half), to nearest even.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& w, float f[8]) {
     f[0] = bf16_lo(w.x); f[1] = bf16_hi(w.x);
     f[2] = bf16_lo(w.y); f[3] = bf16_hi(w.y);

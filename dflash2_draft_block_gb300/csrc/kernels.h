@@ -130,4 +130,55 @@ cudaError_t conv_apply_launch(const void* x, bool f32, int64_t P, int C, int B, 
                               const float* base_io, const float* dyn, int64_t dyn_ld, void* y,
                               cudaStream_t stream, const void* res = nullptr);
 
+// ---- rows of a table by token id (embedding.cu); leading dimensions in elements
+struct EmbeddingArgs {
+    const void* table;
+    bool table_bf16;
+    int64_t ld, V, D;
+    const int32_t* ids;
+    int64_t N;
+    float scale;
+    void* out;
+    bool out_bf16;
+    int64_t out_ld;
+    int32_t* status;
+};
+cudaError_t embedding_launch(const EmbeddingArgs& a, cudaStream_t stream);
+
+// ---- (id, position) pairs of N < 2^31 ids in order of id, then of position
+//      (token_sort.cu): id in the low word, V for an id that is no token (negative, or
+//      outside the table, or of a row whose label is negative), which sort last
+struct SortJob {
+    const int32_t* ids;
+    int64_t N;
+    uint32_t V;
+    const int32_t* label;  // [N / per_label], nullable
+    uint32_t per_label;
+    uint64_t* pairs;       // [N] out
+    uint64_t* spare;       // [N] scratch
+    int32_t* status;
+};
+size_t token_sort_bytes(int64_t N);  // of pairs, and of spare
+cudaError_t token_sort_launch(const SortJob& job, cudaStream_t stream);
+
+// ---- out[v, :] (+)= scale * sum over positions n of token v, in order, of
+//      w[n] * src[n / per_row, :]   (fold.cu)
+struct FoldArgs {
+    const uint64_t* pairs;  // token_sort_launch's
+    int64_t N, V, D;
+    const void* src;
+    bool src_bf16;
+    int64_t src_ld;
+    uint32_t per_row;
+    const float* w;         // nullable (1)
+    float scale;
+    void* out;
+    bool out_bf16;
+    int64_t out_ld;
+    bool accumulate;        // false: rows without a token become zeros
+    float* parts;           // fold_parts_bytes(N, D)
+};
+size_t fold_parts_bytes(int64_t N, int64_t D);
+cudaError_t fold_launch(const FoldArgs& a, cudaStream_t stream);
+
 }  // namespace df2

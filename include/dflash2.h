@@ -15,6 +15,12 @@
  *   dflash2_conv_finish           the same conv after the sublayer
  *   dflash2_conv_finish_prepare   a finish and the next sublayer's prepare in one call
  *
+ * and, for training the selector (each call says where it goes past the pages):
+ *
+ *   dflash2_embedding             rows of a table by token id, scaled
+ *   dflash2_embedding_grad        the table's gradient, by sorted tokens
+ *   dflash2_adamw                 an AdamW step over many tensors
+ *
  * Sources (web pages, cited by title and section):
  *   [vLLM]  "DFlash2", vLLM Speculators user guide: "Local Convolution",
  *           "Candidate Selector", "Key Parameters".
@@ -45,7 +51,8 @@
  * - dev_status (nullable): a device int32 that kernels OR DF2_STATUS_* bits into.
  *   The library never clears it; the caller zeroes it when it wants a fresh read.
  * - Inputs must be finite; NaN/Inf inputs give unspecified ids.
- * - Alignment: every tensor pointer must be 16-byte aligned.
+ * - Alignment: every tensor pointer must be 16-byte aligned, unless the call says that
+ *   its elements' alignment is enough.
  */
 #ifndef DFLASH2_H
 #define DFLASH2_H
@@ -65,7 +72,7 @@ extern "C" {
 #define DF2_ERR_WORKSPACE_TOO_SMALL 4
 #define DF2_ERR_TIMEOUT 5            /* reserved: a bounded device wait gave up */
 
-/* Activation dtypes for the conv calls. */
+/* Dtypes: the conv calls' activations, the training calls' tensors. */
 #define DF2_DTYPE_BF16 0
 #define DF2_DTYPE_F32 1
 
@@ -421,6 +428,98 @@ int dflash2_conv_finish_prepare(const void* z, int dtype, int64_t P, int C, int 
                                 const uint16_t* W_proj, const float* base_next, void* y_next,
                                 float* dyn_out_next, void* workspace, size_t workspace_bytes,
                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_embedding — rows of a table by token id, scaled.
+ *
+ * No counterpart in the pages, which take the drafter's inputs as given: the rows of a
+ * draft block (the anchor token and the mask tokens) or of a packed training batch.
+ *   out[n, :] = scale * table[ids[n], :]        one fp32 product, rounded to out's dtype
+ * A negative id is a position without a token: its row is zeros.  An id >= V sets
+ * DF2_STATUS_ID_OUT_OF_RANGE and its row is NaN.
+ *
+ *   table [V, D] table_dtype, rows table_ld >= D elements apart
+ *   ids   [N]    int32
+ *   out   [N, D] out_dtype, rows out_ld >= D elements apart
+ * Rules: N >= 0, D >= 1, 1 <= V <= DF2_MAX_VOCAB, scale finite; N < 2^31, D <= 2^24 and
+ * N * D <= 2^40 (else DF2_ERR_UNSUPPORTED).  Tensors need only their elements'
+ * alignment; D and strides a multiple of 8 with 16-byte aligned tensors run faster.
+ * ---------------------------------------------------------------------- */
+int dflash2_embedding(const void* table, int table_dtype, int64_t V, int64_t D, int64_t table_ld,
+                      const int32_t* ids, int64_t N, float scale, void* out, int out_dtype, int64_t out_ld,
+                      int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_embedding_grad — the gradient of dflash2_embedding's table.
+ *
+ *   dtable[v, :] (+)= scale * sum over n with ids[n] = v of dout[n, :]
+ * The ids are sorted first, stably; a token's rows are summed in fp32 in an order that
+ * ids and the sizes alone fix, so equal inputs give equal bits, and the sum is rounded
+ * to dtable's dtype once.  accumulate = 0: every row is written, those of absent tokens
+ * as zeros; accumulate != 0: the sums are added to dtable, and rows of absent tokens are
+ * neither read nor written.  Positions with a negative id have no part (their dout is
+ * not read); an id >= V sets DF2_STATUS_ID_OUT_OF_RANGE and has none either.
+ *
+ *   dout   [N, D] dout_dtype, rows dout_ld >= D elements apart
+ *   ids    [N]    int32
+ *   dtable [V, D] dtable_dtype, rows dtable_ld >= D elements apart, out
+ *   workspace      >= dflash2_embedding_grad_workspace_size(N, V, D)
+ * Rules and alignment as for dflash2_embedding; dtable must not overlap dout.
+ * ---------------------------------------------------------------------- */
+size_t dflash2_embedding_grad_workspace_size(int64_t N, int64_t V, int64_t D);
+int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dout_ld, const int32_t* ids, int64_t N,
+                           int64_t V, int64_t D, float scale, int accumulate, void* dtable, int dtable_dtype,
+                           int64_t dtable_ld, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_adamw — one AdamW step (decoupled weight decay) over many tensors.
+ *
+ * No counterpart in the pages, which leave the optimiser open.  For every element of
+ * every tensor, in separately rounded fp32 operations, with t = step:
+ *   g = grad * grad_scale                       (grad_scale NULL: 1)
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * g * g
+ *   w = w * (1 - lr * weight_decay)
+ *       - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * w is `master` where given (param then gets its rounding to param's dtype), else param
+ * itself, rounded to its dtype.
+ *
+ * state_bits 32: exp_avg holds m, exp_avg_2 holds v, fp32, n elements each.
+ * state_bits 8: exp_avg holds m and exp_avg_2 holds sqrt(v), as n e4m3 values each, in
+ * units of one fp32 scale per DF2_ADAMW_BLOCK consecutive elements (exp_avg_scale,
+ * exp_avg_2_scale: ceil(n / DF2_ADAMW_BLOCK) each): value = e4m3 * scale, scale = absmax *
+ * (1 / 448), e4m3 = the value times ((1 / absmax) * 448), to nearest even, every operation
+ * rounded to fp32; sqrt(v) above zero is held as at least 2^-9 scales; a block whose
+ * absmax is below 2^-100 holds zeros with scale 0.  A fresh state is all
+ * zeros, in either form.
+ *
+ *   tensors     host array of `count` descriptors, read before the call returns; the
+ *               pointers in it are device pointers; tensors with n = 0 are skipped
+ *   grad_scale  device fp32 scalar (a clip coefficient, 1 / tokens, a loss scale's
+ *               inverse), nullable.  Where it is NaN or infinite the whole step is left
+ *               out: nothing is written.
+ * Rules: state_bits 32 or 8; 0 <= beta1, beta2 < 1; eps, lr, weight_decay finite and >= 0;
+ * step >= 1 (1 = the first).  Tensors need only their elements' alignment (tensors whose
+ * pointers are all 16-byte aligned run faster); no two buffers may overlap.
+ * ---------------------------------------------------------------------- */
+#define DF2_ADAMW_BLOCK 256
+typedef struct {
+    void* param;              /* [n] param_dtype, in and out */
+    float* master;            /* [n] fp32, in and out, nullable */
+    const void* grad;         /* [n] grad_dtype */
+    void* exp_avg;            /* [n] fp32 or e4m3, in and out */
+    void* exp_avg_2;          /* [n] fp32 or e4m3, in and out */
+    float* exp_avg_scale;     /* [ceil(n / DF2_ADAMW_BLOCK)], state_bits 8 */
+    float* exp_avg_2_scale;   /* the same */
+    int64_t n;
+    int param_dtype;          /* DF2_DTYPE_* */
+    int grad_dtype;
+    double lr;
+    double weight_decay;
+} dflash2_adamw_tensor;
+int dflash2_adamw(const dflash2_adamw_tensor* tensors, int count, int state_bits, double beta1, double beta2,
+                  double eps, int64_t step, const float* grad_scale, void* stream);
 
 /* ------------------------------------------------------------------------
  * dflash2_selftest_wait_timeout — exercises the in-kernel timeout path.
