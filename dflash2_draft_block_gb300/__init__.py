@@ -609,4 +609,67 @@ def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=F
     return out
 
 
+def selector_loss_grad_workspace_size(P, V, K, r) -> int:
+    return int(lib().dflash2_selector_loss_grad_workspace_size(P, V, K, r))
+
+
+def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weights=None, accumulate=False,
+                       dA=True, dBc=True, dtype=torch.float32, workspace=None, dev_status=None, out=None, stream=None):
+    """The selector's K-way loss of the teacher-forced scores and the gradients of
+    sum(row_weights * loss).  Returns (loss [P], label [P] int32, dscores [P, K], dG [P, r],
+    dA [V, r], dBc [V, r]); rows without a candidate target give label -1, NaN loss and
+    contribute nothing.
+
+    dA, dBc: a tensor to write (or with accumulate to add to), True for a new one in
+    `dtype`, None to leave it out.  out: (loss, label, dscores, dG)."""
+    _need(pred, "pred", torch.int32, 1)
+    _need(targets, "targets", torch.int32, 1)
+    _need(topk_ids, "topk_ids", torch.int32)
+    _need(topk_vals, "topk_vals", torch.float32)
+    _need(G, "G", torch.float32)
+    _need(A, "A", torch.bfloat16, 2)
+    _need(Bc, "Bc", torch.bfloat16, 2)
+    P = pred.shape[0]
+    K = topk_ids.shape[-1]
+    V, r = A.shape
+    if targets.shape[0] != P or topk_ids.numel() != P * K or topk_vals.numel() != P * K or G.numel() != P * r:
+        raise ValueError("shapes do not match [P], [P, K], [P, r]")
+    if tuple(Bc.shape) != (V, r):
+        raise ValueError("Bc must be [V, r] like A")
+    if row_weights is not None:
+        _need(row_weights, "row_weights", torch.float32)
+        if row_weights.numel() != P:
+            raise ValueError("row_weights must be [P]")
+    dev = _device(pred, targets=targets, topk_ids=topk_ids, topk_vals=topk_vals, G=G, A=A, Bc=Bc,
+                  row_weights=row_weights)
+    given = [t for t in (dA, dBc) if isinstance(t, torch.Tensor)]
+    if given:
+        dtype = given[0].dtype
+    if dtype not in _DTYPES:
+        raise TypeError(f"dA and dBc must be bfloat16 or float32, got {dtype}")
+    if accumulate and (dA is True or dBc is True):
+        raise ValueError("accumulate adds to dA and dBc: they must be given (None leaves one out)")
+    dA, dBc = (torch.empty((V, r), dtype=dtype, device=dev) if t is True else t for t in (dA, dBc))
+    for name, t in (("dA", dA), ("dBc", dBc)):
+        if t is not None:
+            _out(t, name, dtype, V * r, dev)
+    if out is None:
+        e = torch.empty
+        out = (e((P,), dtype=torch.float32, device=dev), e((P,), dtype=torch.int32, device=dev),
+               e((P, K), dtype=torch.float32, device=dev), e((P, r), dtype=torch.float32, device=dev))
+    loss, label, ds, dG = out
+    _out(loss, "loss", torch.float32, P, dev)
+    _out(label, "label", torch.int32, P, dev)
+    _out(ds, "dscores", torch.float32, P * K, dev)
+    _out(dG, "dG", torch.float32, P * r, dev)
+    _status(dev_status, dev)
+    ws = _scratch(selector_loss_grad_workspace_size(P, V, K, r), workspace, dev, stream)
+    rc = lib().dflash2_selector_loss_grad(
+        _p(pred), _p(targets), P, _p(topk_ids), _p(topk_vals), _p(G), _p(A), _p(Bc), V, K, r, _p(row_weights),
+        int(bool(accumulate)), _p(loss), _p(label), _p(ds), _p(dG), _p(dA), _p(dBc), _DTYPES[dtype], _p(ws),
+        _nbytes(ws), _p(dev_status), _stream(stream, dev))
+    _check("dflash2_selector_loss_grad", rc)
+    return loss, label, ds, dG, dA, dBc
+
+
 from .optim import AdamW  # noqa: E402  (needs the checks above)

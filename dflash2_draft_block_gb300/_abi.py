@@ -53,6 +53,9 @@ SIGNATURES = {
     "dflash2_conv_finish_prepare_workspace_size": (_sz, [_i64, _int, _int, _int, _int]),
     "dflash2_conv_finish_prepare": (_int, [_vp, _int, _i64, _int, _int, _int, _int, _vp, _vp, _vp, _vp, _vp,
                                            _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dflash2_selector_loss_grad_workspace_size": (_sz, [_i64, _i64, _int, _int]),
+    "dflash2_selector_loss_grad": (_int, [_vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _int, _int, _vp, _int, _vp,
+                                          _vp, _vp, _vp, _vp, _vp, _int, _vp, _sz, _vp, _vp]),
     "dflash2_embedding": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _i64, _f32, _vp, _int, _i64, _vp, _vp]),
     "dflash2_embedding_grad_workspace_size": (_sz, [_i64, _i64, _i64]),
     "dflash2_embedding_grad": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _f32, _int, _vp, _int, _i64, _vp, _sz,

@@ -114,3 +114,91 @@ DF2_API int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dou
                ? DF2_OK
                : DF2_ERR_CUDA;
 }
+
+// ---------------------------------------------------------- selector loss --
+
+namespace {
+
+int check_loss(int64_t P, int64_t V, int K, int r) {
+    if (P < 0 || V < 1 || K < 1 || r < 1 || K > V) return DF2_ERR_INVALID_ARGUMENT;
+    if (K > DF2_MAX_TOPK || r > DF2_MAX_RANK || r % 8 != 0 || V > DF2_MAX_VOCAB) return DF2_ERR_UNSUPPORTED;
+    if (P > kMaxPositions / K) return DF2_ERR_UNSUPPORTED;
+    return DF2_OK;
+}
+
+// The rows' u and G * t, then each fold's scratch.
+struct LossSpace {
+    size_t u, gt, fold_b, fold_a, bytes;
+};
+
+LossSpace loss_space(int64_t P, int K, int r) {
+    LossSpace s;
+    const size_t rows = round_up(size_t(P) * r * sizeof(float));
+    s.u = 0;
+    s.gt = rows;
+    s.fold_b = 2 * rows;
+    s.fold_a = s.fold_b + fold_space(P * K, r).bytes;
+    s.bytes = s.fold_a + fold_space(P, r).bytes;
+    return s;
+}
+
+}  // namespace
+
+DF2_API size_t dflash2_selector_loss_grad_workspace_size(int64_t P, int64_t V, int K, int r) {
+    if (check_loss(P, V, K, r) != DF2_OK || P == 0) return 0;
+    return loss_space(P, K, r).bytes;
+}
+
+DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* topk_ids,
+                                       const float* topk_vals, const float* G, const uint16_t* A, const uint16_t* Bc,
+                                       int64_t V, int K, int r, const float* row_weights, int accumulate, float* loss,
+                                       int32_t* label_idx, float* dscores, float* dG, void* dA, void* dBc,
+                                       int table_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                       void* stream) {
+    const int rc = check_loss(P, V, K, r);
+    if (rc != DF2_OK) return rc;
+    if (!dtype_ok(table_dtype) || (dA && dA == dBc)) return DF2_ERR_INVALID_ARGUMENT;
+    if (P > 0 && (!pred || !targets || !topk_ids || !topk_vals || !G || !A || !Bc || !loss || !label_idx || !dscores || !dG))
+        return DF2_ERR_INVALID_ARGUMENT;
+    const void* wide[] = {G, A, Bc, dG, dA, dBc, workspace};
+    for (const void* p : wide)
+        if (reinterpret_cast<uintptr_t>(p) & 15u) return DF2_ERR_UNSUPPORTED;
+    const void* words[] = {pred, targets, topk_ids, topk_vals, row_weights, loss, label_idx, dscores};
+    for (const void* p : words)
+        if (!element_aligned(p, DF2_DTYPE_F32)) return DF2_ERR_UNSUPPORTED;
+    const size_t need = dflash2_selector_loss_grad_workspace_size(P, V, K, r);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return DF2_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    char* base = static_cast<char*>(workspace);
+    const LossSpace s = loss_space(P, K, r);
+    float* u = reinterpret_cast<float*>(base + s.u);
+    float* gt = reinterpret_cast<float*>(base + s.gt);
+    if (P > 0 && df2::selector_loss_launch(pred, targets, P, topk_ids, topk_vals, G, A, Bc, V, K, r, row_weights, loss,
+                                           label_idx, dscores, dG, dBc ? u : nullptr, dA ? gt : nullptr, dev_status,
+                                           st) != cudaSuccess)
+        return DF2_ERR_CUDA;
+    df2::FoldArgs f{};
+    f.V = V;
+    f.D = f.src_ld = f.out_ld = r;
+    f.scale = 1.f;
+    f.out_bf16 = table_dtype == DF2_DTYPE_BF16;
+    f.accumulate = accumulate != 0;
+    if (dBc) {
+        f.N = P * K;
+        f.src = u;
+        f.per_row = uint32_t(K);
+        f.w = dscores;
+        f.out = dBc;
+        if (sort_and_fold(f, topk_ids, label_idx, uint32_t(K), base + s.fold_b, nullptr, st) != cudaSuccess)
+            return DF2_ERR_CUDA;
+    }
+    if (dA) {
+        f.N = P;
+        f.src = gt;
+        f.per_row = 1;
+        f.w = nullptr;
+        f.out = dA;
+        if (sort_and_fold(f, pred, label_idx, 1, base + s.fold_a, nullptr, st) != cudaSuccess) return DF2_ERR_CUDA;
+    }
+    return DF2_OK;
+}

@@ -181,4 +181,12 @@ struct FoldArgs {
 size_t fold_parts_bytes(int64_t N, int64_t D);
 cudaError_t fold_launch(const FoldArgs& a, cudaStream_t stream);
 
+// ---- the selector's loss and gradients, row by row (selector_loss.cu); u [P, r] =
+//      A[pred] * G and gt [P, r] = G * t for the folds into dBc and dA (each nullable),
+//      written for the rows whose label is not -1
+cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
+                                 const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
+                                 int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
+                                 float* u, float* gt, int32_t* status, cudaStream_t stream);
+
 }  // namespace df2

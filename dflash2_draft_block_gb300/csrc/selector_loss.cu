@@ -1,0 +1,290 @@
+// dflash2_selector_loss_grad, the rows: teacher-forced scores, their K-way cross-entropy
+// and every gradient of one row in one pass over its candidates' Bc rows.
+//
+// With a = A[pred], u = a * G and the row weight w:
+//   s_j = val_j + <u, Bc[id_j]>,  loss = log sum exp(s) - s_label
+//   ds_j = w * (softmax(s)_j - [j = label]),  t = sum_j ds_j Bc[id_j]
+//   dG = a * t,  and for the folds into the codebooks' gradients: u (weighted by ds_j, for
+//   dBc[id_j]) and G * t (for dA[pred])
+//
+// One CTA a row, of as many warps as hold the row's K x r bf16 values in 64 registers a
+// lane: a group of L lanes covers r (8 columns a lane and chunk, CH chunks), and a lane
+// keeps KW = 16 / CH candidates.  The values are loaded once, used for the scores and,
+// after the softmax, again for t.  Rows too large for eight warps' registers are walked
+// in rounds and loaded a second time for t.  Scores are summed over a group's lanes by
+// halving: at every step a lane hands half of its candidates to its partner, so KW
+// candidates cost about KW shuffles instead of KW * log2(L).
+//
+// Bound: gathers from L2 and HBM (K rows of 2 r bytes each); all of a row's loads are in
+// flight at once.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace df2 {
+namespace {
+
+constexpr int kMaxWarps = 8;
+constexpr float kNan = __builtin_nanf("");
+
+struct LossArgs {
+    const int32_t* pred;
+    const int32_t* targets;
+    const int32_t* ids;
+    const float* vals;
+    const float* G;
+    const uint16_t* A;
+    const uint16_t* Bc;
+    int64_t V;
+    int K, r;
+    const float* weights;
+    float* loss;
+    int32_t* label;
+    float* ds;
+    float* dG;
+    float* u;
+    float* gt;
+    int32_t* status;
+};
+
+__device__ __forceinline__ float dot8(const uint4& b, const float u[8], float acc) {
+    float f[8];
+    unpack8(b, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc = fmaf(u[i], f[i], acc);
+    return acc;
+}
+
+__device__ __forceinline__ void read8(const float* p, float f[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+__device__ __forceinline__ void write8(float* p, const float f[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Shared memory: u [r], scores [K], t parts [warps][r], one word a warp.
+size_t loss_smem(int warps, int K, int r) { return (size_t(warps + 1) * r + K + kMaxWarps) * 4; }
+
+// L lanes a group, CH chunks of 8 columns a lane (CH > 1 only with L = 32).
+template <int L, int CH>
+__global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const LossArgs a, int rounds) {
+    constexpr int KW = 16 / CH, GROUPS = 32 / L;
+    extern __shared__ float smem[];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int group = lane / L, gl = lane & (L - 1);
+    const int64_t p = blockIdx.x;
+    float* su = smem;
+    float* sc = su + a.r + (size_t(warps) * a.r);  // after the t parts
+    float* st = su + a.r;
+    int* sw = reinterpret_cast<int*>(sc + a.K);
+
+    // the label's column, or none; a bad id anywhere drops the row
+    const int32_t* ids = a.ids + p * a.K;
+    const int32_t y = __ldg(a.targets + p), pr = __ldg(a.pred + p);
+    int col = INT_MAX;
+    bool bad = pr < 0 || pr >= a.V || y >= a.V;
+    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
+        const int32_t id = __ldg(ids + j);
+        bad |= id < 0 || id >= a.V;
+        if (id == y) col = min(col, j);
+    }
+    if (__any_sync(kFull, bad)) col = -1;
+    else col = __reduce_min_sync(kFull, col);
+    if (warps > 1) {
+        if (lane == 0) sw[warp] = col;
+        __syncthreads();
+        for (int w = 0; w < warps; ++w) col = min(col, sw[w]);
+    }
+    if (col == -1 && threadIdx.x == 0 && a.status) atomicOr(a.status, DF2_STATUS_ID_OUT_OF_RANGE);
+    bool live = col >= 0 && col < a.K;
+
+    const float* g = a.G + p * a.r;
+    const uint16_t* arow = a.A + int64_t(live ? pr : 0) * a.r;
+    uint4 b[KW][CH];
+    const int per_round = warps * GROUPS * KW;
+    auto first_of = [&](int round) { return round * per_round + (warp * GROUPS + group) * KW; };
+    auto gather = [&](int round) {
+        const int j0 = first_of(round);
+        int32_t id[KW];
+#pragma unroll
+        for (int k = 0; k < KW; ++k) id[k] = j0 + k < a.K ? __ldg(ids + j0 + k) : -1;
+#pragma unroll
+        for (int k = 0; k < KW; ++k)
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int x = (c * L + gl) * 8;
+                b[k][c] = make_uint4(0, 0, 0, 0);
+                if (id[k] >= 0 && x < a.r) b[k][c] = __ldg(reinterpret_cast<const uint4*>(a.Bc + int64_t(id[k]) * a.r + x));
+            }
+    };
+    if (live) {
+        gather(0);
+        for (int x = threadIdx.x * 8; x < a.r; x += blockDim.x * 8) {
+            float f[8], v[8];
+            unpack8(__ldg(reinterpret_cast<const uint4*>(arow + x)), f);
+            read8(g + x, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= f[i];
+            write8(su + x, v);
+            if (a.u) write8(a.u + p * a.r + x, v);
+        }
+        __syncthreads();
+        for (int round = 0; round < rounds; ++round) {
+            if (round) gather(round);
+            float s[KW];
+#pragma unroll
+            for (int k = 0; k < KW; ++k) s[k] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int x = (c * L + gl) * 8;
+                if (x < a.r) {
+                    float u[8];
+                    read8(su + x, u);
+#pragma unroll
+                    for (int k = 0; k < KW; ++k) s[k] = dot8(b[k][c], u, s[k]);
+                }
+            }
+            int at = first_of(round);
+            int n = KW;
+#pragma unroll
+            for (int o = L / 2; o; o >>= 1) {
+                const bool up = lane & o;
+                if (n > 1) {
+                    n >>= 1;
+#pragma unroll
+                    for (int k = 0; k < KW / 2; ++k) {
+                        if (k >= n) break;
+                        const float send = up ? s[k] : s[k + n], keep = up ? s[k + n] : s[k];
+                        s[k] = keep + __shfl_xor_sync(kFull, send, o);
+                    }
+                    at += up ? n : 0;
+                } else {
+                    s[0] += __shfl_xor_sync(kFull, s[0], o);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KW; ++k)
+                if (k < n && at + k < a.K) sc[at + k] = __ldg(a.vals + p * a.K + at + k) + s[k];
+        }
+        __syncthreads();
+    }
+
+    // softmax over the row's scores, every warp for itself
+    float m = -INFINITY, sum = 0.f;
+    if (live) {
+        for (int j = lane; j < a.K; j += 32) m = fmaxf(m, sc[j]);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        live = m != -INFINITY;  // every candidate masked: nothing to learn
+        if (live) {
+            for (int j = lane; j < a.K; j += 32) sum += expf(sc[j] - m);
+            sum = warp_sum(sum);
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.loss[p] = live ? logf(sum) + m - sc[col] : kNan;
+        a.label[p] = live ? col : -1;
+    }
+    if (!live) {
+        for (int j = threadIdx.x; j < a.K; j += blockDim.x) a.ds[p * a.K + j] = 0.f;
+        for (int x = threadIdx.x; x < a.r; x += blockDim.x) a.dG[p * a.r + x] = 0.f;
+        return;
+    }
+    const float w = a.weights ? __ldg(a.weights + p) : 1.f;
+    auto dscore = [&](int j) { return w * (expf(sc[j] - m) / sum - (j == col ? 1.f : 0.f)); };
+    for (int j = threadIdx.x; j < a.K; j += blockDim.x) a.ds[p * a.K + j] = dscore(j);
+
+    // t: a lane's columns over its candidates, then over groups, rounds and warps
+    for (int round = 0; round < rounds; ++round) {
+        if (rounds > 1) gather(round);
+        const int j0 = first_of(round);
+        float d[KW];
+#pragma unroll
+        for (int k = 0; k < KW; ++k) d[k] = j0 + k < a.K ? dscore(j0 + k) : 0.f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                float f[8];
+                unpack8(b[k][c], f);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[i] = fmaf(d[k], f[i], t[i]);
+            }
+#pragma unroll
+            for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) t[i] += __shfl_xor_sync(kFull, t[i], o);
+            const int x = (c * L + gl) * 8;
+            if (group == 0 && x < a.r) {
+                float* q = st + warp * a.r + x;
+                if (round) {
+                    float f[8];
+                    read8(q, f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) t[i] += f[i];
+                }
+                write8(q, t);
+            }
+        }
+    }
+    __syncthreads();
+    for (int x = threadIdx.x * 8; x < a.r; x += blockDim.x * 8) {
+        float t[8], f[8], v[8];
+        read8(st + x, t);
+        for (int q = 1; q < warps; ++q) {
+            read8(st + q * a.r + x, f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] += f[i];
+        }
+        unpack8(__ldg(reinterpret_cast<const uint4*>(arow + x)), f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = f[i] * t[i];
+        write8(a.dG + p * a.r + x, v);
+        if (a.gt) {
+            read8(g + x, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= t[i];
+            write8(a.gt + p * a.r + x, v);
+        }
+    }
+}
+
+template <int L, int CH>
+cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
+    constexpr int per_warp = 32 / L * (16 / CH);
+    int warps = 1;
+    while (warps < kMaxWarps && warps * per_warp < a.K) warps *= 2;
+    const int rounds = (a.K + warps * per_warp - 1) / (warps * per_warp);
+    const size_t smem = loss_smem(warps, a.K, a.r);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(selector_loss_kernel<L, CH>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+        if (e != cudaSuccess) return e;
+    }
+    selector_loss_kernel<L, CH><<<unsigned(P), warps * 32, smem, stream>>>(a, rounds);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
+                                 const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
+                                 int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
+                                 float* u, float* gt, int32_t* status, cudaStream_t stream) {
+    const LossArgs a{pred, targets, ids, vals, G, A, Bc, V, K, r, weights, loss, label, ds, dG, u, gt, status};
+    if (r <= 32) return launch<4, 1>(a, P, stream);
+    if (r <= 64) return launch<8, 1>(a, P, stream);
+    if (r <= 128) return launch<16, 1>(a, P, stream);
+    if (r <= 256) return launch<32, 1>(a, P, stream);
+    if (r <= 512) return launch<32, 2>(a, P, stream);
+    if (r <= 1024) return launch<32, 4>(a, P, stream);
+    if (r <= 2048) return launch<32, 8>(a, P, stream);
+    return launch<32, 16>(a, P, stream);
+}
+
+}  // namespace df2

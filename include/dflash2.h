@@ -17,6 +17,7 @@
  *
  * and, for training the selector (each call says where it goes past the pages):
  *
+ *   dflash2_selector_loss_grad    the selector's loss and its gradients
  *   dflash2_embedding             rows of a table by token id, scaled
  *   dflash2_embedding_grad        the table's gradient, by sorted tokens
  *   dflash2_adamw                 an AdamW step over many tensors
@@ -428,6 +429,43 @@ int dflash2_conv_finish_prepare(const void* z, int dtype, int64_t P, int C, int 
                                 const uint16_t* W_proj, const float* base_next, void* y_next,
                                 float* dyn_out_next, void* workspace, size_t workspace_bytes,
                                 void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_selector_loss_grad — the selector's training loss with its gradients.
+ *
+ * ([PR62] "Selector training objective"; [vLLM] "Training Objective": the K-way
+ * cross-entropy of the teacher-forced scores; the pages give no gradients, these are the
+ * formula's.)  For row p, with a = A[pred[p]], G = G[p], w = row_weights[p] (NULL: 1):
+ *   u = a * G,   s_j = topk_vals[p, j] + <u, Bc[id_j]>         (dflash2_selector_pair_scores)
+ *   label_idx = the first column j with topk_ids[p, j] == targets[p], else -1
+ *   loss      = log(sum_j exp(s_j)) - s_label                    (dflash2_selector_ce)
+ *   dscores_j = w * (softmax(s)_j - [j == label])    also the gradient of topk_vals
+ *   t = sum_j dscores_j * Bc[id_j];   dG = a * t
+ *   dA[pred[p], :] += G * t;   dBc[id_j, :] += dscores_j * u   for every j
+ * loss is not weighted; the gradients are those of sum_p w_p * loss_p.  A row without a
+ * label (targets[p] < 0 or not a candidate), one with an id outside [0, V) in pred,
+ * targets or topk_ids (which sets DF2_STATUS_ID_OUT_OF_RANGE), and one whose scores are
+ * all -inf contribute nothing: loss NaN, label_idx -1, dscores and dG zero, and their G,
+ * topk_vals and weight are not used.
+ * dA and dBc are summed in fp32 in an order the ids fix and rounded to table_dtype once;
+ * accumulate = 0 writes every row of them, accumulate != 0 adds to the rows of the tokens
+ * that occur, as dflash2_embedding_grad does.  NULL leaves one out (a frozen codebook).
+ *
+ *   pred, targets [P] int32; topk_ids [P, K] int32; topk_vals [P, K] fp32; G [P, r] fp32
+ *   A, Bc [V, r] bf16; row_weights [P] fp32, nullable
+ *   loss [P] fp32, label_idx [P] int32, dscores [P, K] fp32, dG [P, r] fp32   out
+ *   dA, dBc [V, r] table_dtype, out, nullable
+ *   workspace >= dflash2_selector_loss_grad_workspace_size(P, V, K, r)
+ * Rules: P >= 0, 1 <= K <= min(V, DF2_MAX_TOPK), 1 <= r <= DF2_MAX_RANK, r % 8 == 0,
+ * V <= DF2_MAX_VOCAB, P * K < 2^31; outputs must not overlap inputs or one another.
+ * ---------------------------------------------------------------------- */
+size_t dflash2_selector_loss_grad_workspace_size(int64_t P, int64_t V, int K, int r);
+int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* topk_ids,
+                               const float* topk_vals, const float* G, const uint16_t* A, const uint16_t* Bc,
+                               int64_t V, int K, int r, const float* row_weights, int accumulate, float* loss,
+                               int32_t* label_idx, float* dscores, float* dG, void* dA, void* dBc,
+                               int table_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                               void* stream);
 
 /* ------------------------------------------------------------------------
  * dflash2_embedding — rows of a table by token id, scaled.
