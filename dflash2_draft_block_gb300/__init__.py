@@ -63,10 +63,15 @@ def _on_device(t):
 def _stream(stream, device):
     """The CUDA stream handle of `stream` (default: the current one), which must
     belong to the device of the call's tensors."""
+    if stream is None and _raw_stream is not None and device.index is not None:
+        return ct.c_void_p(_raw_stream(device.index))  # the handle alone, in a tenth of the time
     s = stream if stream is not None else torch.cuda.current_stream()
     if s.device != device:
         raise ValueError(f"the stream is on {s.device}, the call's tensors on {device}")
     return ct.c_void_p(s.cuda_stream)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _need(t, name, dtype, ndim=None):

@@ -41,19 +41,11 @@ FoldSpace fold_space(int64_t N, int64_t D) {
     return s;
 }
 
-// Sorts the ids into the scratch at base and folds (a's tensors and sizes are set).
-cudaError_t sort_and_fold(df2::FoldArgs a, const int32_t* ids, const int32_t* label, uint32_t per_label, char* base,
-                          int32_t* status, cudaStream_t stream) {
-    const FoldSpace s = fold_space(a.N, a.D);
-    if (a.N > 0) {
-        df2::SortJob j{ids, a.N, uint32_t(a.V), label, per_label, reinterpret_cast<uint64_t*>(base + s.pairs),
-                       reinterpret_cast<uint64_t*>(base + s.spare), status};
-        const cudaError_t e = df2::token_sort_launch(j, stream);
-        if (e != cudaSuccess) return e;
-    }
-    a.pairs = reinterpret_cast<const uint64_t*>(base + s.pairs);
-    a.parts = reinterpret_cast<float*>(base + s.parts);
-    return df2::fold_launch(a, stream);
+void set_space(df2::FoldArgs* a, char* base) {
+    const FoldSpace s = fold_space(a->N, a->D);
+    a->pairs = reinterpret_cast<uint64_t*>(base + s.pairs);
+    a->spare = reinterpret_cast<uint64_t*>(base + s.spare);
+    a->parts = reinterpret_cast<float*>(base + s.parts);
 }
 
 }  // namespace
@@ -97,6 +89,7 @@ DF2_API int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dou
     const size_t need = dflash2_embedding_grad_workspace_size(N, V, D);
     if (workspace_bytes < need || (need > 0 && !workspace)) return DF2_ERR_WORKSPACE_TOO_SMALL;
     df2::FoldArgs a{};
+    a.ids = ids;
     a.N = N;
     a.V = V;
     a.D = D;
@@ -109,10 +102,11 @@ DF2_API int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dou
     a.out_bf16 = dtable_dtype == DF2_DTYPE_BF16;
     a.out_ld = dtable_ld;
     a.accumulate = accumulate != 0;
-    return sort_and_fold(a, ids, nullptr, 1, static_cast<char*>(workspace), dev_status,
-                         static_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? DF2_OK
-               : DF2_ERR_CUDA;
+    a.status = dev_status;
+    set_space(&a, static_cast<char*>(workspace));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (df2::fold_sort_launch(&a, 1, st) != cudaSuccess) return DF2_ERR_CUDA;
+    return df2::fold_launch(&a, 1, st) == cudaSuccess ? DF2_OK : DF2_ERR_CUDA;
 }
 
 // ---------------------------------------------------------- selector loss --
@@ -173,32 +167,35 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
     const LossSpace s = loss_space(P, K, r);
     float* u = reinterpret_cast<float*>(base + s.u);
     float* gt = reinterpret_cast<float*>(base + s.gt);
+    df2::FoldArgs jobs[2];
+    int count = 0;
+    auto add = [&](void* out, const int32_t* ids, int64_t N, const float* src, size_t space) {
+        if (!out) return static_cast<df2::FoldArgs*>(nullptr);
+        df2::FoldArgs& f = jobs[count++] = df2::FoldArgs{};
+        f.ids = ids;
+        f.N = N;
+        f.V = V;
+        f.D = f.src_ld = f.out_ld = r;
+        f.src = src;
+        f.per_row = 1;
+        f.scale = 1.f;
+        f.out = out;
+        f.out_bf16 = table_dtype == DF2_DTYPE_BF16;
+        f.accumulate = accumulate != 0;
+        set_space(&f, base + space);
+        return &f;
+    };
+    if (df2::FoldArgs* f = add(dBc, topk_ids, P * K, u, s.fold_b)) {
+        f->w = dscores;  // zero where a row was dropped
+        f->per_row = uint32_t(K);
+    }
+    if (df2::FoldArgs* f = add(dA, pred, P, gt, s.fold_a)) f->label = label_idx;
+    // the ids alone decide the sort: the rows run beside it
+    if (count && P > 0 && df2::fold_sort_launch(jobs, count, st) != cudaSuccess) return DF2_ERR_CUDA;
     if (P > 0 && df2::selector_loss_launch(pred, targets, P, topk_ids, topk_vals, G, A, Bc, V, K, r, row_weights, loss,
                                            label_idx, dscores, dG, dBc ? u : nullptr, dA ? gt : nullptr, dev_status,
-                                           st) != cudaSuccess)
+                                           count && df2::fold_sorts(jobs, count), st) != cudaSuccess)
         return DF2_ERR_CUDA;
-    df2::FoldArgs f{};
-    f.V = V;
-    f.D = f.src_ld = f.out_ld = r;
-    f.scale = 1.f;
-    f.out_bf16 = table_dtype == DF2_DTYPE_BF16;
-    f.accumulate = accumulate != 0;
-    if (dBc) {
-        f.N = P * K;
-        f.src = u;
-        f.per_row = uint32_t(K);
-        f.w = dscores;
-        f.out = dBc;
-        if (sort_and_fold(f, topk_ids, label_idx, uint32_t(K), base + s.fold_b, nullptr, st) != cudaSuccess)
-            return DF2_ERR_CUDA;
-    }
-    if (dA) {
-        f.N = P;
-        f.src = gt;
-        f.per_row = 1;
-        f.w = nullptr;
-        f.out = dA;
-        if (sort_and_fold(f, pred, label_idx, 1, base + s.fold_a, nullptr, st) != cudaSuccess) return DF2_ERR_CUDA;
-    }
+    if (count && df2::fold_launch(jobs, count, st) != cudaSuccess) return DF2_ERR_CUDA;
     return DF2_OK;
 }

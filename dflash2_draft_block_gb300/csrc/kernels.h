@@ -147,46 +147,56 @@ cudaError_t embedding_launch(const EmbeddingArgs& a, cudaStream_t stream);
 
 // ---- (id, position) pairs of N < 2^31 ids in order of id, then of position
 //      (token_sort.cu): id in the low word, V for an id that is no token (negative, or
-//      outside the table, or of a row whose label is negative), which sort last
+//      outside the table), which sort last
+constexpr int kMaxJobs = 2;  // lists a launch
 struct SortJob {
     const int32_t* ids;
     int64_t N;
     uint32_t V;
-    const int32_t* label;  // [N / per_label], nullable
-    uint32_t per_label;
     uint64_t* pairs;       // [N] out
     uint64_t* spare;       // [N] scratch
     int32_t* status;
 };
 size_t token_sort_bytes(int64_t N);  // of pairs, and of spare
-cudaError_t token_sort_launch(const SortJob& job, cudaStream_t stream);
+cudaError_t token_sort_launch(const SortJob* jobs, int count, cudaStream_t stream);
 
 // ---- out[v, :] (+)= scale * sum over positions n of token v, in order, of
 //      w[n] * src[n / per_row, :]   (fold.cu)
 struct FoldArgs {
-    const uint64_t* pairs;  // token_sort_launch's
+    const int32_t* ids;     // [N]; ids outside [0, V) are no tokens
     int64_t N, V, D;
     const void* src;
     bool src_bf16;
     int64_t src_ld;
     uint32_t per_row;
-    const float* w;         // nullable (1)
+    const float* w;         // [N], nullable (1); positions of weight 0 are not read
+    const int32_t* label;   // [N / per_row], nullable; rows of a negative label are not read
     float scale;
     void* out;
     bool out_bf16;
     int64_t out_ld;
     bool accumulate;        // false: rows without a token become zeros
-    float* parts;           // fold_parts_bytes(N, D)
+    int32_t* status;
+    uint64_t* pairs;        // [N] scratch each (token_sort_bytes), and fold_parts_bytes(N, D)
+    uint64_t* spare;
+    float* parts;
 };
 size_t fold_parts_bytes(int64_t N, int64_t D);
-cudaError_t fold_launch(const FoldArgs& a, cudaStream_t stream);
+// Folds of one call: equal types of src and of out.  fold_sort_launch orders the positions,
+// fold_launch does the rest; a kernel between them may overlap the first (it must not
+// depend on it) and may write src, w and label.
+bool fold_sorts(const FoldArgs* jobs, int count);  // whether fold_sort_launch launches anything
+cudaError_t fold_sort_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
+cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
 
 // ---- the selector's loss and gradients, row by row (selector_loss.cu); u [P, r] =
 //      A[pred] * G and gt [P, r] = G * t for the folds into dBc and dA (each nullable),
-//      written for the rows whose label is not -1
+//      written for the rows whose label is not -1.  beside: the launch before this one is
+//      the sort of the same call, and the rows may start beside it
 cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
                                  const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
                                  int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
-                                 float* u, float* gt, int32_t* status, cudaStream_t stream);
+                                 float* u, float* gt, int32_t* status, bool beside,
+                                 cudaStream_t stream);
 
 }  // namespace df2

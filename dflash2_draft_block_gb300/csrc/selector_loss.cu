@@ -44,15 +44,24 @@ struct LossArgs {
     float* u;
     float* gt;
     int32_t* status;
+    bool beside;  // launched to run beside the kernel before it
 };
 
-__device__ __forceinline__ float dot8(const uint4& b, const float u[8], float acc) {
-    float f[8];
-    unpack8(b, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) acc = fmaf(u[i], f[i], acc);
-    return acc;
+// Two fp32 in a register pair, and two fused multiply-adds in one instruction.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
 }
+__device__ __forceinline__ void split2(uint64_t d, float* lo, float* hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t w) { return pair2(bf16_lo(w), bf16_hi(w)); }
 
 __device__ __forceinline__ void read8(const float* p, float f[8]) {
     const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
@@ -63,6 +72,12 @@ __device__ __forceinline__ void read8(const float* p, float f[8]) {
 __device__ __forceinline__ void write8(float* p, const float f[8]) {
     *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// A kernel that ran beside the one before it ends after it (its block 0 does), so that what
+// follows in the stream finds both complete.
+__device__ __forceinline__ void end_after_previous(const LossArgs& a) {
+    if (a.beside && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Shared memory: u [r], scores [K], t parts [warps][r], one word a warp.
@@ -135,17 +150,29 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
         for (int round = 0; round < rounds; ++round) {
             if (round) gather(round);
             float s[KW];
+            uint64_t s2[KW];
 #pragma unroll
-            for (int k = 0; k < KW; ++k) s[k] = 0.f;
+            for (int k = 0; k < KW; ++k) s2[k] = 0;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 const int x = (c * L + gl) * 8;
                 if (x < a.r) {
-                    float u[8];
-                    read8(su + x, u);
+                    const ulonglong2 u01 = *reinterpret_cast<const ulonglong2*>(su + x);
+                    const ulonglong2 u23 = *reinterpret_cast<const ulonglong2*>(su + x + 4);
 #pragma unroll
-                    for (int k = 0; k < KW; ++k) s[k] = dot8(b[k][c], u, s[k]);
+                    for (int k = 0; k < KW; ++k) {
+                        s2[k] = fma2(bf16_pair(b[k][c].x), u01.x, s2[k]);
+                        s2[k] = fma2(bf16_pair(b[k][c].y), u01.y, s2[k]);
+                        s2[k] = fma2(bf16_pair(b[k][c].z), u23.x, s2[k]);
+                        s2[k] = fma2(bf16_pair(b[k][c].w), u23.y, s2[k]);
+                    }
                 }
+            }
+#pragma unroll
+            for (int k = 0; k < KW; ++k) {
+                float lo, hi;
+                split2(s2[k], &lo, &hi);
+                s[k] = lo + hi;
             }
             int at = first_of(round);
             int n = KW;
@@ -184,18 +211,24 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
             sum = warp_sum(sum);
         }
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0) {  // (before the scores give way below)
         a.loss[p] = live ? logf(sum) + m - sc[col] : kNan;
         a.label[p] = live ? col : -1;
     }
     if (!live) {
         for (int j = threadIdx.x; j < a.K; j += blockDim.x) a.ds[p * a.K + j] = 0.f;
         for (int x = threadIdx.x; x < a.r; x += blockDim.x) a.dG[p * a.r + x] = 0.f;
+        end_after_previous(a);
         return;
     }
     const float w = a.weights ? __ldg(a.weights + p) : 1.f;
-    auto dscore = [&](int j) { return w * (expf(sc[j] - m) / sum - (j == col ? 1.f : 0.f)); };
-    for (int j = threadIdx.x; j < a.K; j += blockDim.x) a.ds[p * a.K + j] = dscore(j);
+    __syncthreads();  // every warp has its maximum and sum: the scores give way to dscores
+    for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
+        const float d = w * (expf(sc[j] - m) / sum - (j == col ? 1.f : 0.f));
+        sc[j] = d;
+        a.ds[p * a.K + j] = d;
+    }
+    __syncthreads();
 
     // t: a lane's columns over its candidates, then over groups, rounds and warps
     for (int round = 0; round < rounds; ++round) {
@@ -203,17 +236,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
         const int j0 = first_of(round);
         float d[KW];
 #pragma unroll
-        for (int k = 0; k < KW; ++k) d[k] = j0 + k < a.K ? dscore(j0 + k) : 0.f;
+        for (int k = 0; k < KW; ++k) d[k] = j0 + k < a.K ? sc[j0 + k] : 0.f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
-            float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint64_t t2[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
-                float f[8];
-                unpack8(b[k][c], f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = fmaf(d[k], f[i], t[i]);
+                const uint64_t dd = pair2(d[k], d[k]);
+                t2[0] = fma2(bf16_pair(b[k][c].x), dd, t2[0]);
+                t2[1] = fma2(bf16_pair(b[k][c].y), dd, t2[1]);
+                t2[2] = fma2(bf16_pair(b[k][c].z), dd, t2[2]);
+                t2[3] = fma2(bf16_pair(b[k][c].w), dd, t2[3]);
             }
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split2(t2[i], &t[2 * i], &t[2 * i + 1]);
 #pragma unroll
             for (int o = L; o < 32; o <<= 1)
 #pragma unroll
@@ -251,6 +288,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
             write8(a.gt + p * a.r + x, v);
         }
     }
+    end_after_previous(a);
 }
 
 template <int L, int CH>
@@ -265,9 +303,19 @@ cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
-    selector_loss_kernel<L, CH><<<unsigned(P), warps * 32, smem, stream>>>(a, rounds);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned(P));
+    cfg.blockDim = dim3(unsigned(warps * 32));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.beside ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, selector_loss_kernel<L, CH>, a, rounds);
     note_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace
@@ -275,8 +323,8 @@ cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
 cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
                                  const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
                                  int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
-                                 float* u, float* gt, int32_t* status, cudaStream_t stream) {
-    const LossArgs a{pred, targets, ids, vals, G, A, Bc, V, K, r, weights, loss, label, ds, dG, u, gt, status};
+                                 float* u, float* gt, int32_t* status, bool beside, cudaStream_t stream) {
+    const LossArgs a{pred, targets, ids, vals, G, A, Bc, V, K, r, weights, loss, label, ds, dG, u, gt, status, beside};
     if (r <= 32) return launch<4, 1>(a, P, stream);
     if (r <= 64) return launch<8, 1>(a, P, stream);
     if (r <= 128) return launch<16, 1>(a, P, stream);
