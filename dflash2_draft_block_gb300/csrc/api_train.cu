@@ -27,9 +27,9 @@ int check_rows(int64_t N, int64_t V, int64_t D) {
     return DF2_OK;
 }
 
-// One fold's scratch: the sorted pairs, their other half, the parts.
+// One fold's scratch: the sorted pairs, their other half, the parts, the split tokens.
 struct FoldSpace {
-    size_t pairs, spare, parts, bytes;
+    size_t pairs, spare, parts, split, bytes;
 };
 
 FoldSpace fold_space(int64_t N, int64_t D) {
@@ -37,7 +37,8 @@ FoldSpace fold_space(int64_t N, int64_t D) {
     s.pairs = 0;
     s.spare = round_up(df2::token_sort_bytes(N));
     s.parts = 2 * s.spare;
-    s.bytes = s.parts + round_up(df2::fold_parts_bytes(N, D));
+    s.split = s.parts + round_up(df2::fold_parts_bytes(N, D));
+    s.bytes = s.split + round_up(df2::fold_split_bytes(N, D));
     return s;
 }
 
@@ -46,6 +47,7 @@ void set_space(df2::FoldArgs* a, char* base) {
     a->pairs = reinterpret_cast<uint64_t*>(base + s.pairs);
     a->spare = reinterpret_cast<uint64_t*>(base + s.spare);
     a->parts = reinterpret_cast<float*>(base + s.parts);
+    a->split = reinterpret_cast<uint32_t*>(base + s.split);
 }
 
 }  // namespace

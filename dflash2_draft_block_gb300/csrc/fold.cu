@@ -7,12 +7,17 @@
 // writes a token's row when the list moves on to the next.  A token that runs over a
 // chunk's end is finished by the group it began in when less than E / 2 positions are left
 // of it; a longer one (a mask token can hold most of a batch) is split there, every chunk
-// leaves its part in fp32, and fold_join_kernel adds the parts, one CTA a (token, slice).
-// Where the cuts fall depends on the sorted list alone, so results repeat bit for bit.
+// leaves its part in fp32, the group the token began in notes it down, and
+// fold_join_kernel adds the parts, one CTA a (token, slice) at a time.  Where the cuts fall
+// depends on the sorted list alone, so results repeat bit for bit.  Four rows in flight and
+// 96 registers leave five CTAs an SM (eight rows take 122 and leave four).
 //
-// Without accumulate the rows of absent tokens become zeros: further CTAs of the same launch
-// each take a range of rows, mark those that the sorted list holds, and clear the others,
-// so every row is written once, and the writes run beside the gathers.
+// Without accumulate the rows of absent tokens become zeros in the same launch: 152 CTAs
+// from the start, and the others when their chunks are done, take ranges of rows off a
+// counter, mark those that the sorted list holds, and clear the others, so every row is
+// written once, and the writes run beside the gathers.  (With fill CTAs spread among the
+// others the folds had a third of the SMs' room; with a fixed share each, one CTA an SM wrote
+// 4.1 TB/s.)
 //
 // Lists of up to kSmall positions are not sorted at all: every position looks for its equals
 // in the list itself, the first of them owns the token (fold_small_kernel).
@@ -26,11 +31,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kAhead = 8;
+constexpr int kAhead = 4;  // rows in flight a lane
 constexpr int kJoinWarps = 4;
+constexpr int kJoinBlocks = 152 * 4;  // at most: each takes split tokens in turn
 constexpr int kSmall = 512;
-constexpr int kFillRows = 4096;       // rows a fill CTA takes at most
-constexpr int64_t kFillBytes = 512 * 1024;  // and the bytes, while the CTAs fill the SMs eight times
+constexpr int kFillRows = 4096;          // rows a fill takes at a time, at most
+constexpr int kZeros = 4096;              // bytes of zeros a fill CTA copies from
+constexpr int64_t kFillBytes = 128 * 1024;  // and the bytes
+constexpr int kFillBlocks = 152;          // CTAs that only fill, the first of a launch
 
 struct Plan {
     FoldArgs a[kMaxJobs];
@@ -39,18 +47,14 @@ struct Plan {
     int64_t chunks[kMaxJobs];
     int slices[kMaxJobs];
     int fold_blocks[kMaxJobs];
-    int fill_blocks[kMaxJobs];
+    int fills[kMaxJobs];      // ranges of fill_rows rows
+    int fill_blocks;          // CTAs that do nothing else
     int fill_rows[kMaxJobs];
     int fill_unit[kMaxJobs];  // bytes a store
 };
 
 __device__ __forceinline__ uint32_t key_at(const uint64_t* pairs, int64_t i) {
     return uint32_t(__ldg(pairs + i));
-}
-
-// Whether the token that ends chunk [.., b) goes on for at least half positions from b.
-__device__ __forceinline__ bool split_at(const uint64_t* pairs, int64_t N, int64_t b, int half) {
-    return b + half <= N && key_at(pairs, b - 1) == key_at(pairs, b + half - 1);
 }
 
 template <int L>
@@ -125,21 +129,35 @@ struct Row {
     }
 };
 
-// out[row, lane's columns] = scale * f (+ itself).  Added in fp32 by the memory's own add:
-// a row has one writer, so the result is the one rounded sum, and nobody waits for the old
-// row (the add flushes subnormal operands).
+// Where a lane writes its columns of a row, and how.
+struct Out {
+    char* p;         // row 0 at the lane's first column
+    uint64_t stride;  // bytes a row
+    int64_t left;    // columns from there on
+    float scale;
+    bool accumulate;
+};
+
+template <int W, int L>
+__device__ __forceinline__ Out out_of(const FoldArgs& a, int64_t slice, int gl) {
+    const int sz = a.out_bf16 ? 2 : 4;
+    const int64_t c = column<W, L>(slice, gl, 0);
+    return Out{static_cast<char*>(a.out) + c * sz, uint64_t(a.out_ld) * sz, a.D - c, a.scale, a.accumulate};
+}
+
+// A row's columns = scale * f (+ themselves).  Added in fp32 by the memory's own add: a row
+// has one writer, so the result is the one rounded sum, and nobody waits for the old row
+// (the add flushes subnormal operands).
 template <bool OUT16, int W, int L>
-__device__ __forceinline__ void put_row(const FoldArgs& a, int64_t row, int64_t slice, int gl, const float f[8]) {
-    constexpr int SZ = OUT16 ? 2 : 4;
-    char* p = static_cast<char*>(a.out) + (row * a.out_ld + column<W, L>(slice, gl, 0)) * SZ;
-    float g[8];
+__device__ __forceinline__ void put_columns(char* p, int64_t left, float scale, bool accumulate, float4 x, float4 y) {
+    float g[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(f[i], a.scale);
+    for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(g[i], scale);
     if (W == 8) {
-        if (column<W, L>(slice, gl, 0) >= a.D) return;
+        if (left <= 0) return;
         if (OUT16) {
             uint4* q = reinterpret_cast<uint4*>(p);
-            if (a.accumulate) {
+            if (accumulate) {
                 float o[8];
                 unpack8(*q, o);
 #pragma unroll
@@ -148,8 +166,9 @@ __device__ __forceinline__ void put_row(const FoldArgs& a, int64_t row, int64_t 
             *q = make_uint4(pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3]), pack_bf16(g[4], g[5]), pack_bf16(g[6], g[7]));
         } else {
             float4* q = reinterpret_cast<float4*>(p);
-            const float4 x = make_float4(g[0], g[1], g[2], g[3]), y = make_float4(g[4], g[5], g[6], g[7]);
-            if (a.accumulate) {
+            x = make_float4(g[0], g[1], g[2], g[3]);
+            y = make_float4(g[4], g[5], g[6], g[7]);
+            if (accumulate) {
                 atomicAdd(q, x);
                 atomicAdd(q + 1, y);
             } else {
@@ -159,25 +178,40 @@ __device__ __forceinline__ void put_row(const FoldArgs& a, int64_t row, int64_t 
         }
     } else if (OUT16) {
         uint16_t* q = reinterpret_cast<uint16_t*>(p);
-        if (a.accumulate) {
+        if (accumulate) {
             uint16_t o[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[i] = column<W, L>(slice, gl, i) < a.D ? q[i * L] : uint16_t(0);
+            for (int i = 0; i < 8; ++i) o[i] = i * L < left ? q[i * L] : uint16_t(0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] = __fadd_rn(bf16_to_f32(o[i]), g[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (column<W, L>(slice, gl, i) < a.D) q[i * L] = f32_to_bf16_rn(g[i]);
+            if (i * L < left) q[i * L] = f32_to_bf16_rn(g[i]);
     } else {
         float* q = reinterpret_cast<float*>(p);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (column<W, L>(slice, gl, i) >= a.D) continue;
-            if (a.accumulate) atomicAdd(q + i * L, g[i]);
+            if (i * L >= left) continue;
+            if (accumulate) atomicAdd(q + i * L, g[i]);
             else q[i * L] = g[i];
         }
     }
+}
+
+template <bool OUT16, int W, int L>
+__device__ __noinline__ void put_columns_call(char* p, int64_t left, float scale, bool accumulate, float4 x, float4 y) {
+    put_columns<OUT16, W, L>(p, left, scale, accumulate, x, y);
+}
+
+// Column by column a row takes so much code that the copies of it in the fold's loop cost
+// more in instruction fetches than a call does (52 against 31 us for 5003 rows of 251);
+// with vectors the call costs more (95 against 76 us for 262,144 rows of 256).
+template <bool OUT16, int W, int L>
+__device__ __forceinline__ void put_row(const Out& o, uint32_t row, const float f[8]) {
+    const float4 x = make_float4(f[0], f[1], f[2], f[3]), y = make_float4(f[4], f[5], f[6], f[7]);
+    if (W == 8) put_columns<OUT16, W, L>(o.p + row * o.stride, o.left, o.scale, o.accumulate, x, y);
+    else put_columns_call<OUT16, W, L>(o.p + row * o.stride, o.left, o.scale, o.accumulate, x, y);
 }
 
 // (a weight of one adds f as it is)
@@ -198,12 +232,17 @@ __device__ __forceinline__ float4* part_at(const FoldArgs& a, int64_t slices, in
     return reinterpret_cast<float4*>(a.parts + ((c * 2 + s) * slices + slice) * (8 * L) + gl * 8);
 }
 
-// Zeros to the rows [block * fill_rows, ..) of absent tokens.
+// 1-D bulk copy shared -> global of `bytes` (a multiple of 16; both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(uint32_t(__cvta_generic_to_shared(src))), "r"(bytes)
+                 : "memory");
+}
+
+// Zeros to the rows [block * fill_rows, ..) of a job's absent tokens.
 template <bool SMALL>
-__device__ void fill(const Plan& p, int job, int64_t block) {
-    __shared__ uint32_t held[kFillRows / 32];
-    __shared__ int64_t range[2];
-    const FoldArgs& a = p.a[job];
+__device__ void fill(const Plan& p, int job, int64_t block, uint32_t* held, int64_t* range, const uint4* zeros) {
+    const FoldArgs a = job ? p.a[1] : p.a[0];  // (a parameter indexed by a register is slow to read)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t v0 = block * p.fill_rows[job];
     const int rows = int(dmin<int64_t>(p.fill_rows[job], a.V - v0));
@@ -242,6 +281,14 @@ __device__ void fill(const Plan& p, int job, int64_t block) {
     const int sz = a.out_bf16 ? 2 : 4, unit = p.fill_unit[job];
     const int64_t ld = a.out_ld * sz, per = a.D * sz / unit;
     char* out = static_cast<char*>(a.out) + v0 * ld;
+    if (unit == 16) {  // a bulk copy of zeros a row
+        for (int r = tid; r < rows; r += kThreads) {
+            if (held[r >> 5] >> (r & 31) & 1) continue;
+            for (int64_t o = 0; o < per * 16; o += kZeros) bulk_store(out + r * ld + o, zeros, uint32_t(dmin<int64_t>(kZeros, per * 16 - o)));
+        }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        return;
+    }
     // lanes across a row; several rows a warp where a row has few units
     int across = 32;
     while (across > 1 && across / 2 >= per) across /= 2;
@@ -249,46 +296,53 @@ __device__ void fill(const Plan& p, int job, int64_t block) {
     for (int r = tid / across; r < rows; r += stride) {
         if (held[r >> 5] >> (r & 31) & 1) continue;
         char* q = out + r * ld;
-        if (unit == 16)
-            for (int64_t i = sub; i < per; i += across) reinterpret_cast<uint4*>(q)[i] = make_uint4(0, 0, 0, 0);
-        else if (unit == 4)
+        if (unit == 4)
             for (int64_t i = sub; i < per; i += across) reinterpret_cast<uint32_t*>(q)[i] = 0;
         else
             for (int64_t i = sub; i < per; i += across) reinterpret_cast<uint16_t*>(q)[i] = 0;
     }
 }
 
-// A block's part in a launch of all jobs' folds and fills, the two kinds spread evenly: the
-// job and the block's number there; fill: which kind.
-__device__ __forceinline__ int64_t part_of(const Plan& p, int* job, bool* fill) {
-    int64_t folds = 0, fills = 0;
-    for (int j = 0; j < p.count; ++j) {
-        folds += p.fold_blocks[j];
-        fills += p.fill_blocks[j];
+// The CTA's share of all jobs' fills: ranges off the counter while there are any, or the
+// range of its number.
+template <bool SMALL>
+__device__ void fill_all(const Plan& p) {
+    __shared__ uint32_t held[kFillRows / 32];
+    __shared__ int64_t range[2];
+    __shared__ __align__(16) uint4 zeros[kZeros / 16];
+    __shared__ int taken;
+    const int total = p.fills[0] + p.fills[1];
+    if (total == 0) return;
+    for (int i = threadIdx.x; i < kZeros / 16; i += kThreads) zeros[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // for the copies that read them
+    for (;;) {
+        int u = blockIdx.x;
+        if (!SMALL) {
+            if (threadIdx.x == 0) taken = int(dmin(atomicAdd(p.a[0].split + 1, 1u), uint32_t(total)));
+            __syncthreads();
+            u = taken;
+            if (u >= total) break;
+        }
+        const int job = u >= p.fills[0];
+        fill<SMALL>(p, job, u - (job ? p.fills[0] : 0), held, range, zeros);
+        if (SMALL) break;
+        __syncthreads();
     }
-    const int64_t b = blockIdx.x, before = b * fills / (folds + fills);
-    *fill = (b + 1) * fills / (folds + fills) > before;
-    int64_t n = *fill ? before : b - before;
-    const int* blocks = *fill ? p.fill_blocks : p.fold_blocks;
-    *job = 0;
-    if (p.count > 1 && n >= blocks[0]) {
-        n -= blocks[0];
-        *job = 1;
-    }
-    return n;
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+// A fold CTA's job and its number there.
+__device__ __forceinline__ int64_t fold_block(const Plan& p, int* job) {
+    const int64_t n = int64_t(blockIdx.x) - p.fill_blocks;
+    *job = n >= p.fold_blocks[0];
+    return *job ? n - p.fold_blocks[0] : n;
+}
+
+// A group's chunk and slice.
 template <bool SRC16, bool OUT16, int W, int L>
-__global__ void __launch_bounds__(kThreads) fold_kernel(const __grid_constant__ Plan p) {
-    // the join may take its place now: it waits for this kernel where it reads parts
-    asm volatile("griddepcontrol.launch_dependents;");
+__device__ __forceinline__ void fold_chunk(const Plan& p) {
     int job;
-    bool is_fill;
-    const int64_t block = part_of(p, &job, &is_fill);
-    if (is_fill) {
-        fill<false>(p, job, block);
-        return;
-    }
+    const int64_t block = fold_block(p, &job);
     const FoldArgs& a = p.a[job];
     const int lane = threadIdx.x & 31, gl = lane & (L - 1);
     const unsigned gmask = group_mask<L>(lane);
@@ -298,29 +352,36 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const __grid_constant__ 
     if (c >= p.chunks[job]) return;
     const uint64_t* pairs = a.pairs;
     const int64_t e0 = c * E, e1 = dmin<int64_t>(e0 + E, a.N);
+    // the keys that decide where this group's tokens begin and end, in one round of loads:
+    // before and at each end of the chunk, and half a chunk from it
+    const int64_t probe = gl < 3 ? (gl == 0 ? e0 - 1 : gl == 1 ? e0 : e0 + half - 1)
+                                 : (gl == 3 ? e1 - 1 : gl == 4 ? e1 : e1 + half - 1);
+    const bool held = gl < 6 && probe >= 0 && probe < a.N;
+    const uint64_t probed = held ? __ldg(pairs + probe) : ~uint64_t(0);
+    const uint32_t pk = held ? uint32_t(probed) : 0xFFFFFFFFu;  // (no token is that)
+    auto probed_key = [&](int k) { return __shfl_sync(gmask, pk, k, L); };
+    const uint32_t k_before = probed_key(0), k_first = probed_key(1), k_last = probed_key(3);
+    const bool crosses0 = k_before == k_first, crosses1 = k_last == probed_key(4);
+    bool head = crosses0 && probed_key(2) == k_before;
+    const bool tail = crosses1 && probed_key(5) == k_last;
     int64_t i = e0, end = e1;
-    bool head = false, tail = false;
-    if (c > 0 && key_at(pairs, e0 - 1) == key_at(pairs, e0)) {
-        head = split_at(pairs, a.N, e0, half);
-        if (!head) i = run_end<L>(pairs, a.N, e0, half, lane);
-    }
+    if (crosses0 && !head) i = run_end<L>(pairs, a.N, e0, half, lane);
     if (i >= e1) return;  // a short last chunk the one before it finishes
-    if (e1 < a.N && key_at(pairs, e1 - 1) == key_at(pairs, e1)) {
-        tail = split_at(pairs, a.N, e1, half);
-        if (!tail) end = run_end<L>(pairs, a.N, e1, half, lane);
-    }
+    if (crosses1 && !tail) end = run_end<L>(pairs, a.N, e1, half, lane);
 
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const uint32_t none = uint32_t(a.V);
-    uint32_t cur = key_at(pairs, i);
+    const uint64_t begin = __ldg(pairs + i);
+    uint32_t cur = uint32_t(begin);
     if (cur == none) return;
+    const Out o = out_of<W, L>(a, slice, gl);
     auto leave = [&](bool is_tail) {  // the current token's sums, to its row or to its part
         if (head || is_tail) {
             float4* q = part_at<L>(a, slices, c, head ? 0 : 1, slice, gl);
             q[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
             q[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         } else {
-            put_row<OUT16, W, L>(a, cur, slice, gl, acc);
+            put_row<OUT16, W, L>(o, cur, acc);
         }
         head = false;
 #pragma unroll
@@ -329,9 +390,11 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const __grid_constant__ 
     const int64_t left = a.D - column<W, L>(slice, gl, 0);
     const char* src = static_cast<const char*>(a.src) + column<W, L>(slice, gl, 0) * (SRC16 ? 2 : 4);
     const uint64_t stride = uint64_t(a.src_ld) * (SRC16 ? 2 : 4);
+    auto pairs_from = [&](int64_t at) { return at + gl < end ? __ldg(pairs + at + gl) : uint64_t(none); };
+    uint64_t pair = pairs_from(i);
     for (bool more = true; more && i < end; i += L) {
         const int n = int(dmin<int64_t>(L, end - i));
-        const uint64_t pair = gl < n ? __ldg(pairs + i + gl) : uint64_t(none);
+        const uint64_t next = pairs_from(i + L);
         const uint32_t key = uint32_t(pair);
         float w = 0.f;
         const bool on = key != none && counts(a, uint32_t(pair >> 32), &w);
@@ -362,59 +425,65 @@ __global__ void __launch_bounds__(kThreads) fold_kernel(const __grid_constant__ 
                 }
             }
         }
+        pair = next;
     }
-    if (cur != none) leave(tail);
+    if (cur == none) return;
+    // a token that began here and goes on: the join adds its parts
+    if (tail && !head && gl == 0) a.split[2 + atomicAdd(a.split, 1u)] = uint32_t(unit);
+    leave(tail);
+}
+
+template <bool SRC16, bool OUT16, int W, int L>
+__global__ void __launch_bounds__(kThreads, 5) fold_kernel(const __grid_constant__ Plan p) {
+    // the join may take its place now: it waits for this kernel where it reads parts
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (blockIdx.x >= p.fill_blocks) fold_chunk<SRC16, OUT16, W, L>(p);
+    __syncthreads();
+    fill_all<false>(p);
 }
 
 template <bool OUT16, int W, int L>
 __global__ void __launch_bounds__(kJoinWarps * 32) fold_join_kernel(const __grid_constant__ Plan p) {
-    __shared__ float4 sums[kJoinWarps * 32 / L][2][L];
-    // Who owns a split token shows in the sorted list, which was complete before the fold
-    // began; only the parts have to be waited for.  Block 0 always waits, so that this
-    // kernel does not end before the fold.
-    const int64_t units0 = p.chunks[0] * p.slices[0];
-    const int job = blockIdx.x >= units0;
-    const int64_t unit = blockIdx.x - (job ? units0 : 0);
-    const FoldArgs& a = p.a[job];
-    const int slices = p.slices[job], E = p.E[job], half = E / 2;
-    const int64_t c = unit / slices, slice = unit - c * slices;
-    const int64_t e0 = c * E, e1 = e0 + E;
-    uint32_t k = 0;
-    bool owner = e1 < a.N;
-    if (owner) {
-        k = key_at(a.pairs, e1 - 1);
-        // the chunk the token begins in owns the sum
-        owner = k != uint32_t(a.V) && split_at(a.pairs, a.N, e1, half) &&
-                !(c > 0 && key_at(a.pairs, e0 - 1) == k);
-    }
-    if (owner || blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!owner) return;
     constexpr int kGroups = kJoinWarps * 32 / L;
+    __shared__ float4 sums[kGroups][2][L];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int gl = threadIdx.x & (L - 1), group = threadIdx.x / L;
-    int more = 0;  // the chunks after c that left a part
-    for (int got = kJoinWarps * 32; got == kJoinWarps * 32;) {
-        const int64_t b = (c + 1 + more + threadIdx.x) * E;
-        got = __syncthreads_count(b < a.N && key_at(a.pairs, b - 1) == k && split_at(a.pairs, a.N, b, half));
-        more += got;
-    }
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const uint32_t count0 = __ldcg(p.a[0].split), count1 = p.count > 1 ? __ldcg(p.a[1].split) : 0u;
+    for (uint32_t s = blockIdx.x; s < count0 + count1; s += gridDim.x) {
+        const int job = s >= count0;
+        const FoldArgs& a = p.a[job];
+        const uint32_t unit = __ldcg(a.split + 2 + s - (job ? count0 : 0u));
+        const int slices = p.slices[job], E = p.E[job], half = E / 2;
+        const int64_t c = unit / slices, slice = unit - c * slices;
+        const uint32_t k = key_at(a.pairs, (c + 1) * E - 1);
+        int more = 0;  // the chunks after c that left a part
+        for (int got = kJoinWarps * 32; got == kJoinWarps * 32;) {
+            const int64_t b = (c + 1 + more + threadIdx.x) * E;
+            // (a token that reaches half a chunk past b was split at b)
+            got = __syncthreads_count(b + half <= a.N && key_at(a.pairs, b + half - 1) == k);
+            more += got;
+        }
+        float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int m = group; m <= more; m += kGroups) {
-        const float4* q = part_at<L>(a, slices, c + m, m == 0 ? 1 : 0, slice, gl);
-        const float4 x = __ldcg(q), y = __ldcg(q + 1);
-        acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-        acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+        for (int m = group; m <= more; m += kGroups) {
+            const float4* q = part_at<L>(a, slices, c + m, m == 0 ? 1 : 0, slice, gl);
+            const float4 x = __ldcg(q), y = __ldcg(q + 1);
+            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+        }
+        sums[group][0][gl] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        sums[group][1][gl] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        __syncthreads();
+        if (group == 0) {
+            for (int g = 1; g < dmin(kGroups, more + 1); ++g) {
+                const float4 x = sums[g][0][gl], y = sums[g][1][gl];
+                acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+                acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+            }
+            put_row<OUT16, W, L>(out_of<W, L>(a, slice, gl), k, acc);
+        }
+        __syncthreads();
     }
-    sums[group][0][gl] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    sums[group][1][gl] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    __syncthreads();
-    if (group) return;
-    for (int g = 1; g < dmin(kGroups, more + 1); ++g) {
-        const float4 x = sums[g][0][gl], y = sums[g][1][gl];
-        acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-        acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
-    }
-    put_row<OUT16, W, L>(a, k, slice, gl, acc);
 }
 
 // A block a (position, slice).  The block of a token's first position sums the token: the
@@ -422,14 +491,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fold_join_kernel(const __grid
 template <bool SRC16, bool OUT16, int W>
 __global__ void __launch_bounds__(kThreads) fold_small_kernel(const __grid_constant__ Plan p) {
     __shared__ float4 sums[kWarps][2][32];
-    int job;
-    bool is_fill;
-    const int64_t block = part_of(p, &job, &is_fill);
-    if (is_fill) {
-        fill<true>(p, job, block);
+    if (blockIdx.x < p.fill_blocks) {
+        fill_all<true>(p);
         return;
     }
-    const FoldArgs& a = p.a[job];
+    int job;
+    const int64_t block = fold_block(p, &job);
+    const FoldArgs a = job ? p.a[1] : p.a[0];  // (a parameter indexed by a register is slow to read)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int n = int(block / p.slices[job]);
     const int64_t slice = block - int64_t(n) * p.slices[job];
@@ -491,7 +559,7 @@ __global__ void __launch_bounds__(kThreads) fold_small_kernel(const __grid_const
         acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
         acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
     }
-    put_row<OUT16, W, 32>(a, id, slice, lane, acc);
+    put_row<OUT16, W, 32>(out_of<W, 32>(a, slice, lane), uint32_t(id), acc);
 }
 
 // Lanes a group: D up to 64 columns fits eight.
@@ -529,7 +597,7 @@ cudaError_t launch(Plan& p, bool small, int64_t blocks, cudaStream_t stream) {
     const int64_t units = p.chunks[0] * p.slices[0] + (p.count > 1 ? p.chunks[1] * p.slices[1] : 0);
     if (e != cudaSuccess || units == 0) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(units));
+    cfg.gridDim = dim3(unsigned(dmin<int64_t>(units, kJoinBlocks)));
     cfg.blockDim = dim3(kJoinWarps * 32);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -549,13 +617,19 @@ size_t fold_parts_bytes(int64_t N, int64_t D) {
     return size_t((N + E - 1) / E) * 2 * slices_of(D, L) * 8 * L * sizeof(float);
 }
 
+size_t fold_split_bytes(int64_t N, int64_t D) {
+    const int L = lanes_of(D), E = chunk_of(N, D, L);
+    return (2 + size_t((N + E - 1) / E) * slices_of(D, L)) * sizeof(uint32_t);
+}
+
 bool fold_sorts(const FoldArgs* jobs, int count) { return !all_small(jobs, count); }
 
 cudaError_t fold_sort_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
     if (!fold_sorts(jobs, count)) return cudaSuccess;
     SortJob s[kMaxJobs];
     for (int i = 0; i < count; ++i)
-        s[i] = SortJob{jobs[i].ids, jobs[i].N, uint32_t(jobs[i].V), jobs[i].pairs, jobs[i].spare, jobs[i].status};
+        s[i] = SortJob{jobs[i].ids, jobs[i].N, uint32_t(jobs[i].V), jobs[i].pairs, jobs[i].spare, jobs[i].split,
+                       jobs[i].status};
     return token_sort_launch(s, count, stream);
 }
 
@@ -565,7 +639,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
     const bool small = all_small(jobs, count);
     const int L = small ? 32 : lanes_of(jobs[0].D);
     bool vec = true;
-    int64_t blocks = 0;
+    int64_t blocks = 0, fills = 0;
     for (int i = 0; i < count; ++i) {
         const FoldArgs& a = p.a[i] = jobs[i];
         vec = vec && vectors(a.src, a.src_ld, a.D, a.src_bf16) && vectors(a.out, a.out_ld, a.D, a.out_bf16);
@@ -578,16 +652,19 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
             const int64_t sz = a.out_bf16 ? 2 : 4, row = a.D * sz;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row % 16 == 0 && (a.out_ld * sz) % 16 == 0;
             p.fill_unit[i] = wide ? 16 : int(sz);
-            int64_t rows = dmax<int64_t>(1, dmin<int64_t>(kFillRows, kFillBytes / row));
-            rows = dmin(rows, dmax<int64_t>(1, a.V / (152 * 8)));
-            p.fill_rows[i] = int(rows);
+            const int64_t rows = dmin<int64_t>(dmin<int64_t>(kFillRows, kFillBytes / row), a.V / (kFillBlocks * 8));
+            p.fill_rows[i] = int(dmax<int64_t>(1, rows));
             fill = (a.V + p.fill_rows[i] - 1) / p.fill_rows[i];
         }
         if (fold > INT32_MAX || fill > INT32_MAX || p.chunks[i] * p.slices[i] > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
         p.fold_blocks[i] = int(fold);
-        p.fill_blocks[i] = int(fill);
-        blocks += fold + fill;
+        p.fills[i] = int(fill);
+        blocks += fold;
+        fills += fill;
     }
+    if (fills > INT32_MAX) return cudaErrorInvalidConfiguration;
+    p.fill_blocks = int(small ? fills : dmin<int64_t>(fills, kFillBlocks));
+    blocks += p.fill_blocks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     const bool s16 = jobs[0].src_bf16, o16 = jobs[0].out_bf16;

@@ -155,6 +155,7 @@ struct SortJob {
     uint32_t V;
     uint64_t* pairs;       // [N] out
     uint64_t* spare;       // [N] scratch
+    uint32_t* zero;        // two words that become 0
     int32_t* status;
 };
 size_t token_sort_bytes(int64_t N);  // of pairs, and of spare
@@ -177,11 +178,13 @@ struct FoldArgs {
     int64_t out_ld;
     bool accumulate;        // false: rows without a token become zeros
     int32_t* status;
-    uint64_t* pairs;        // [N] scratch each (token_sort_bytes), and fold_parts_bytes(N, D)
-    uint64_t* spare;
+    uint64_t* pairs;        // [N] scratch each (token_sort_bytes), fold_parts_bytes(N, D) and
+    uint64_t* spare;        // fold_split_bytes(N, D)
     float* parts;
+    uint32_t* split;        // how many tokens were split, the fills' counter, then the tokens
 };
 size_t fold_parts_bytes(int64_t N, int64_t D);
+size_t fold_split_bytes(int64_t N, int64_t D);
 // Folds of one call: equal types of src and of out.  fold_sort_launch orders the positions,
 // fold_launch does the rest; a kernel between them may overlap the first (it must not
 // depend on it) and may write src, w and label.
