@@ -14,6 +14,7 @@ contiguous and row-major; calls are asynchronous on the current torch stream.
 from __future__ import annotations
 
 import ctypes as ct
+import functools
 
 import torch
 
@@ -537,11 +538,13 @@ def _rows(t, name, shape=None, dev=None):
     dt = _DTYPES.get(t.dtype)
     if dt is None:
         raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be {'a matrix' if shape is None else list(shape)}, got {list(t.shape)}")
     if dev is not None and t.device != dev:
         raise ValueError(f"{name} is on {t.device}, the call's tensors on {dev}")
     rows, cols = t.shape
+    if t.is_contiguous():
+        return dt, max(cols, 1)
     ld = t.stride(0) if rows > 1 else max(cols, 1)
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError(f"{name} must have dense rows")
@@ -550,11 +553,20 @@ def _rows(t, name, shape=None, dev=None):
 
 def _scratch(nbytes, workspace, dev, stream):
     """The caller's workspace, or one of this call's own, which the allocator keeps from
-    other uses until the kernels of `stream` have read it."""
-    ws = _workspace(nbytes, workspace, dev)
-    if workspace is None and ws is not None and stream is not None:
+    other uses until the kernels of `stream` have read it: (tensor, address, bytes)."""
+    if workspace is not None:
+        ws = _workspace(nbytes, workspace, dev)
+        return ws, ws.data_ptr(), _nbytes(ws)
+    if nbytes == 0:
+        return None, 0, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if stream is not None:
         ws.record_stream(stream)
-    return ws
+    return ws, ws.data_ptr(), nbytes
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else 0
 
 
 def embedding(table, ids, *, scale=1.0, dtype=None, dev_status=None, out=None, stream=None):
@@ -567,23 +579,31 @@ def embedding(table, ids, *, scale=1.0, dtype=None, dev_status=None, out=None, s
     N = ids.numel()
     dev = _device(table, ids=ids)
     if out is None:
-        out = torch.empty((*ids.shape, D), dtype=table.dtype if dtype is None else dtype, device=dev)
-        odt, old = _DTYPES.get(out.dtype), D
+        dtype = table.dtype if dtype is None else dtype
+        odt, old = _DTYPES.get(dtype), D
         if odt is None:
-            raise TypeError(f"dtype must be bfloat16 or float32, got {out.dtype}")
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+        out = torch.empty((*ids.shape, D), dtype=dtype, device=dev)
     else:
         odt, old = _rows(out, "out", (N, D), dev)
         if dtype is not None and dtype != out.dtype:
             raise TypeError(f"out must be {dtype}, got {out.dtype}")
-    _status(dev_status, dev)
-    rc = lib().dflash2_embedding(_p(table), dt, V, D, ld, _p(ids), N, float(scale), _p(out), odt, old,
-                                 _p(dev_status), _stream(stream, dev))
+    if dev_status is not None:
+        _status(dev_status, dev)
+    rc = lib().dflash2_embedding(table.data_ptr(), dt, V, D, ld, ids.data_ptr(), N, scale, out.data_ptr(), odt, old,
+                                 _ptr(dev_status), _stream(stream, dev))
     _check("dflash2_embedding", rc)
     return out
 
 
+@functools.lru_cache(maxsize=256)
+def _size(library, query, *shape):
+    """A workspace query's answer for a shape (it depends on nothing else)."""
+    return int(getattr(library, query)(*shape))
+
+
 def embedding_grad_workspace_size(N, V, D) -> int:
-    return int(lib().dflash2_embedding_grad_workspace_size(N, V, D))
+    return _size(lib(), "dflash2_embedding_grad_workspace_size", N, V, D)
 
 
 def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=False, workspace=None,
@@ -596,26 +616,31 @@ def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=F
     if isinstance(dout, torch.Tensor) and dout.dim() != 2 and dout.dim() == ids.dim() + 1 and dout.is_contiguous():
         dout = dout.view(N, dout.shape[-1])
     dt, ld = _rows(dout, "dout")
-    D = dout.shape[1]
-    if dout.shape[0] != N:
-        raise ValueError(f"dout must have a row an id ({N}), got {dout.shape[0]}")
+    rows, D = dout.shape
+    if rows != N:
+        raise ValueError(f"dout must have a row an id ({N}), got {rows}")
     V = int(V)
     dev = _device(dout, ids=ids)
     if out is None:
         if accumulate:
             raise ValueError("accumulate adds to out: out must be given")
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
         out = torch.empty((V, D), dtype=dtype, device=dev)
-    odt, old = _rows(out, "out", (V, D), dev)
-    _status(dev_status, dev)
-    ws = _scratch(embedding_grad_workspace_size(N, V, D), workspace, dev, stream)
-    rc = lib().dflash2_embedding_grad(_p(dout), dt, ld, _p(ids), N, V, D, float(scale), int(bool(accumulate)),
-                                      _p(out), odt, old, _p(ws), _nbytes(ws), _p(dev_status), _stream(stream, dev))
+        odt, old = _DTYPES[dtype], max(D, 1)
+    else:
+        odt, old = _rows(out, "out", (V, D), dev)
+    if dev_status is not None:
+        _status(dev_status, dev)
+    _ws, ws, nbytes = _scratch(embedding_grad_workspace_size(N, V, D), workspace, dev, stream)
+    rc = lib().dflash2_embedding_grad(dout.data_ptr(), dt, ld, ids.data_ptr(), N, V, D, scale, bool(accumulate),
+                                      out.data_ptr(), odt, old, ws, nbytes, _ptr(dev_status), _stream(stream, dev))
     _check("dflash2_embedding_grad", rc)
     return out
 
 
 def selector_loss_grad_workspace_size(P, V, K, r) -> int:
-    return int(lib().dflash2_selector_loss_grad_workspace_size(P, V, K, r))
+    return _size(lib(), "dflash2_selector_loss_grad_workspace_size", P, V, K, r)
 
 
 def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weights=None, accumulate=False,
@@ -654,25 +679,30 @@ def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weig
         raise TypeError(f"dA and dBc must be bfloat16 or float32, got {dtype}")
     if accumulate and (dA is True or dBc is True):
         raise ValueError("accumulate adds to dA and dBc: they must be given (None leaves one out)")
-    dA, dBc = (torch.empty((V, r), dtype=dtype, device=dev) if t is True else t for t in (dA, dBc))
     for name, t in (("dA", dA), ("dBc", dBc)):
-        if t is not None:
+        if t is not None and t is not True:
             _out(t, name, dtype, V * r, dev)
+    e = torch.empty
+    if dA is True:
+        dA = e((V, r), dtype=dtype, device=dev)
+    if dBc is True:
+        dBc = e((V, r), dtype=dtype, device=dev)
     if out is None:
-        e = torch.empty
-        out = (e((P,), dtype=torch.float32, device=dev), e((P,), dtype=torch.int32, device=dev),
-               e((P, K), dtype=torch.float32, device=dev), e((P, r), dtype=torch.float32, device=dev))
-    loss, label, ds, dG = out
-    _out(loss, "loss", torch.float32, P, dev)
-    _out(label, "label", torch.int32, P, dev)
-    _out(ds, "dscores", torch.float32, P * K, dev)
-    _out(dG, "dG", torch.float32, P * r, dev)
-    _status(dev_status, dev)
-    ws = _scratch(selector_loss_grad_workspace_size(P, V, K, r), workspace, dev, stream)
+        loss, label = e((P,), dtype=torch.float32, device=dev), e((P,), dtype=torch.int32, device=dev)
+        ds, dG = e((P, K), dtype=torch.float32, device=dev), e((P, r), dtype=torch.float32, device=dev)
+    else:
+        loss, label, ds, dG = out
+        _out(loss, "loss", torch.float32, P, dev)
+        _out(label, "label", torch.int32, P, dev)
+        _out(ds, "dscores", torch.float32, P * K, dev)
+        _out(dG, "dG", torch.float32, P * r, dev)
+    if dev_status is not None:
+        _status(dev_status, dev)
+    _ws, ws, nbytes = _scratch(selector_loss_grad_workspace_size(P, V, K, r), workspace, dev, stream)
     rc = lib().dflash2_selector_loss_grad(
-        _p(pred), _p(targets), P, _p(topk_ids), _p(topk_vals), _p(G), _p(A), _p(Bc), V, K, r, _p(row_weights),
-        int(bool(accumulate)), _p(loss), _p(label), _p(ds), _p(dG), _p(dA), _p(dBc), _DTYPES[dtype], _p(ws),
-        _nbytes(ws), _p(dev_status), _stream(stream, dev))
+        pred.data_ptr(), targets.data_ptr(), P, topk_ids.data_ptr(), topk_vals.data_ptr(), G.data_ptr(), A.data_ptr(),
+        Bc.data_ptr(), V, K, r, _ptr(row_weights), bool(accumulate), loss.data_ptr(), label.data_ptr(), ds.data_ptr(),
+        dG.data_ptr(), _ptr(dA), _ptr(dBc), _DTYPES[dtype], ws, nbytes, _ptr(dev_status), _stream(stream, dev))
     _check("dflash2_selector_loss_grad", rc)
     return loss, label, ds, dG, dA, dBc
 

@@ -104,6 +104,7 @@ DF2_API int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dou
     a.out_bf16 = dtable_dtype == DF2_DTYPE_BF16;
     a.out_ld = dtable_ld;
     a.accumulate = accumulate != 0;
+    a.fill = !a.accumulate;
     a.status = dev_status;
     set_space(&a, static_cast<char*>(workspace));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -170,6 +171,7 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
     float* u = reinterpret_cast<float*>(base + s.u);
     float* gt = reinterpret_cast<float*>(base + s.gt);
     df2::FoldArgs jobs[2];
+    df2::ZeroArgs zero{};
     int count = 0;
     auto add = [&](void* out, const int32_t* ids, int64_t N, const float* src, size_t space) {
         if (!out) return static_cast<df2::FoldArgs*>(nullptr);
@@ -184,6 +186,12 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
         f.out = out;
         f.out_bf16 = table_dtype == DF2_DTYPE_BF16;
         f.accumulate = accumulate != 0;
+        // the rows' kernel leaves the memory bus idle and clears the tables meanwhile
+        f.fill = !f.accumulate && P == 0;
+        if (!f.accumulate) {
+            zero.p[count - 1] = static_cast<char*>(out);
+            zero.bytes[count - 1] = V * r * (f.out_bf16 ? 2 : 4);
+        }
         set_space(&f, base + space);
         return &f;
     };
@@ -195,7 +203,7 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
     // the ids alone decide the sort: the rows run beside it
     if (count && P > 0 && df2::fold_sort_launch(jobs, count, st) != cudaSuccess) return DF2_ERR_CUDA;
     if (P > 0 && df2::selector_loss_launch(pred, targets, P, topk_ids, topk_vals, G, A, Bc, V, K, r, row_weights, loss,
-                                           label_idx, dscores, dG, dBc ? u : nullptr, dA ? gt : nullptr, dev_status,
+                                           label_idx, dscores, dG, dBc ? u : nullptr, dA ? gt : nullptr, zero, dev_status,
                                            count && df2::fold_sorts(jobs, count), st) != cudaSuccess)
         return DF2_ERR_CUDA;
     if (count && df2::fold_launch(jobs, count, st) != cudaSuccess) return DF2_ERR_CUDA;

@@ -51,6 +51,14 @@ __device__ __forceinline__ void unpack8(const uint4& w, float f[8]) {
     f[6] = bf16_lo(w.w); f[7] = bf16_hi(w.w);
 }
 
+// 1-D bulk copy shared -> global of `bytes` (a multiple of 16; both addresses 16-byte
+// aligned), in the thread's current bulk group.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+                 "r"(uint32_t(__cvta_generic_to_shared(src))), "r"(bytes)
+                 : "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);

@@ -12,7 +12,7 @@
 // depends on the sorted list alone, so results repeat bit for bit.  Four rows in flight and
 // 96 registers leave five CTAs an SM (eight rows take 122 and leave four).
 //
-// Without accumulate the rows of absent tokens become zeros in the same launch: 152 CTAs
+// Where asked (fill), the rows of absent tokens become zeros in the same launch: 152 CTAs
 // from the start, and the others when their chunks are done, take ranges of rows off a
 // counter, mark those that the sorted list holds, and clear the others, so every row is
 // written once, and the writes run beside the gathers.  (With fill CTAs spread among the
@@ -32,7 +32,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kAhead = 4;  // rows in flight a lane
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 8;
 constexpr int kJoinBlocks = 152 * 4;  // at most: each takes split tokens in turn
 constexpr int kSmall = 512;
 constexpr int kFillRows = 4096;          // rows a fill takes at a time, at most
@@ -230,13 +230,6 @@ __device__ __forceinline__ bool counts(const FoldArgs& a, uint32_t n, float* w) 
 template <int L>
 __device__ __forceinline__ float4* part_at(const FoldArgs& a, int64_t slices, int64_t c, int s, int64_t slice, int gl) {
     return reinterpret_cast<float4*>(a.parts + ((c * 2 + s) * slices + slice) * (8 * L) + gl * 8);
-}
-
-// 1-D bulk copy shared -> global of `bytes` (a multiple of 16; both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(uint32_t(__cvta_generic_to_shared(src))), "r"(bytes)
-                 : "memory");
 }
 
 // Zeros to the rows [block * fill_rows, ..) of a job's absent tokens.
@@ -648,7 +641,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
         p.chunks[i] = (a.N + p.E[i] - 1) / p.E[i];
         const int64_t fold = small ? a.N * p.slices[i] : (p.chunks[i] * p.slices[i] * L + kThreads - 1) / kThreads;
         int64_t fill = 0;
-        if (!a.accumulate) {
+        if (a.fill) {
             const int64_t sz = a.out_bf16 ? 2 : 4, row = a.D * sz;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row % 16 == 0 && (a.out_ld * sz) % 16 == 0;
             p.fill_unit[i] = wide ? 16 : int(sz);

@@ -176,7 +176,8 @@ struct FoldArgs {
     void* out;
     bool out_bf16;
     int64_t out_ld;
-    bool accumulate;        // false: rows without a token become zeros
+    bool accumulate;
+    bool fill;              // rows without a token become zeros (else they are left alone)
     int32_t* status;
     uint64_t* pairs;        // [N] scratch each (token_sort_bytes), fold_parts_bytes(N, D) and
     uint64_t* spare;        // fold_split_bytes(N, D)
@@ -192,6 +193,13 @@ bool fold_sorts(const FoldArgs* jobs, int count);  // whether fold_sort_launch l
 cudaError_t fold_sort_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
 cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
 
+// ---- up to two buffers to clear beside a kernel's own work (16-byte aligned, multiples of
+//      16 bytes; 0: none)
+struct ZeroArgs {
+    char* p[2];
+    int64_t bytes[2];
+};
+
 // ---- the selector's loss and gradients, row by row (selector_loss.cu); u [P, r] =
 //      A[pred] * G and gt [P, r] = G * t for the folds into dBc and dA (each nullable),
 //      written for the rows whose label is not -1.  beside: the launch before this one is
@@ -199,7 +207,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
 cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
                                  const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
                                  int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
-                                 float* u, float* gt, int32_t* status, bool beside,
+                                 float* u, float* gt, const ZeroArgs& zero, int32_t* status, bool beside,
                                  cudaStream_t stream);
 
 }  // namespace df2

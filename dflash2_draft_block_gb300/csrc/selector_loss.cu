@@ -17,6 +17,10 @@
 //
 // Bound: gathers from L2 and HBM (K rows of 2 r bytes each); all of a row's loads are in
 // flight at once.
+//
+// Gradient tables that are to be written whole are cleared here: every CTA sends its share
+// as bulk copies of zeros before its row, which costs the rows little (they wait for gathers
+// from L2, the copies for HBM), and the folds then write the rows of tokens only.
 #include "common.cuh"
 #include "kernels.h"
 
@@ -43,6 +47,8 @@ struct LossArgs {
     float* dG;
     float* u;
     float* gt;
+    ZeroArgs zero;
+    int64_t P;
     int32_t* status;
     bool beside;  // launched to run beside the kernel before it
 };
@@ -74,13 +80,38 @@ __device__ __forceinline__ void write8(float* p, const float f[8]) {
     *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// A kernel that ran beside the one before it ends after it (its block 0 does), so that what
-// follows in the stream finds both complete.
-__device__ __forceinline__ void end_after_previous(const LossArgs& a) {
+constexpr int kZeroBytes = 4096;  // of one copy
+constexpr int kZeroBlocks = 152 * 4;  // CTAs that clear, at least (where there is enough to do)
+
+__host__ __device__ __forceinline__ int64_t zero_units(const ZeroArgs& z, int i) {
+    return (z.bytes[i] + kZeroBytes - 1) / kZeroBytes;
+}
+
+// The CTA's share of the clearing, sent off by one thread; zeros: kZeroBytes of shared memory.
+__device__ __forceinline__ void send_zeros(const ZeroArgs& z, float* zeros) {
+    const int64_t n0 = zero_units(z, 0), n = n0 + zero_units(z, 1);
+    if (n == 0) return;
+    for (int i = threadIdx.x * 4; i < kZeroBytes / 4; i += blockDim.x * 4)
+        *reinterpret_cast<float4*>(zeros + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x) return;
+    for (int64_t u = blockIdx.x * n / gridDim.x, end = (blockIdx.x + 1) * n / gridDim.x; u < end; ++u) {
+        const int i = u >= n0;
+        const int64_t at = (u - (i ? n0 : 0)) * kZeroBytes;
+        bulk_store(z.p[i] + at, zeros, uint32_t(dmin<int64_t>(kZeroBytes, z.bytes[i] - at)));
+    }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// The end of a CTA: its copies have read their zeros; and a kernel that ran beside the one before it ends
+// after it (its block 0 does), so that what follows in the stream finds both complete.
+__device__ __forceinline__ void finish(const LossArgs& a) {
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     if (a.beside && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Shared memory: u [r], scores [K], t parts [warps][r], one word a warp.
+// Shared memory: zeros (where there is something to clear), u [r], scores [K], t parts [warps][r], one word a warp.
 size_t loss_smem(int warps, int K, int r) { return (size_t(warps + 1) * r + K + kMaxWarps) * 4; }
 
 // L lanes a group, CH chunks of 8 columns a lane (CH > 1 only with L = 32).
@@ -91,7 +122,13 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int group = lane / L, gl = lane & (L - 1);
     const int64_t p = blockIdx.x;
-    float* su = smem;
+    const bool clears = a.zero.bytes[0] + a.zero.bytes[1] > 0;
+    float* su = smem + (clears ? kZeroBytes / 4 : 0);
+    send_zeros(a.zero, smem);
+    if (p >= a.P) {
+        finish(a);
+        return;
+    }
     float* sc = su + a.r + (size_t(warps) * a.r);  // after the t parts
     float* st = su + a.r;
     int* sw = reinterpret_cast<int*>(sc + a.K);
@@ -218,7 +255,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
     if (!live) {
         for (int j = threadIdx.x; j < a.K; j += blockDim.x) a.ds[p * a.K + j] = 0.f;
         for (int x = threadIdx.x; x < a.r; x += blockDim.x) a.dG[p * a.r + x] = 0.f;
-        end_after_previous(a);
+        finish(a);
         return;
     }
     const float w = a.weights ? __ldg(a.weights + p) : 1.f;
@@ -288,7 +325,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
             write8(a.gt + p * a.r + x, v);
         }
     }
-    end_after_previous(a);
+    finish(a);
 }
 
 template <int L, int CH>
@@ -297,14 +334,16 @@ cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
     int warps = 1;
     while (warps < kMaxWarps && warps * per_warp < a.K) warps *= 2;
     const int rounds = (a.K + warps * per_warp - 1) / (warps * per_warp);
-    const size_t smem = loss_smem(warps, a.K, a.r);
+    const int64_t zeros = zero_units(a.zero, 0) + zero_units(a.zero, 1);
+    const size_t smem = loss_smem(warps, a.K, a.r) + (zeros ? kZeroBytes : 0);
+    const int64_t blocks = dmax(P, dmin<int64_t>(zeros, kZeroBlocks));
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(selector_loss_kernel<L, CH>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(P));
+    cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(unsigned(warps * 32));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -323,8 +362,9 @@ cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
 cudaError_t selector_loss_launch(const int32_t* pred, const int32_t* targets, int64_t P, const int32_t* ids,
                                  const float* vals, const float* G, const uint16_t* A, const uint16_t* Bc, int64_t V,
                                  int K, int r, const float* weights, float* loss, int32_t* label, float* ds, float* dG,
-                                 float* u, float* gt, int32_t* status, bool beside, cudaStream_t stream) {
-    const LossArgs a{pred, targets, ids, vals, G, A, Bc, V, K, r, weights, loss, label, ds, dG, u, gt, status, beside};
+                                 float* u, float* gt, const ZeroArgs& zero, int32_t* status, bool beside,
+                                 cudaStream_t stream) {
+    const LossArgs a{pred, targets, ids, vals, G, A, Bc, V, K, r, weights, loss, label, ds, dG, u, gt, zero, P, status, beside};
     if (r <= 32) return launch<4, 1>(a, P, stream);
     if (r <= 64) return launch<8, 1>(a, P, stream);
     if (r <= 128) return launch<16, 1>(a, P, stream);

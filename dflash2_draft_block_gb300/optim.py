@@ -155,9 +155,9 @@ class AdamW:
             self._ptrs, self._bound = ptrs, list(grads)
         if not self.params:
             return
-        s = _pkg._stream(stream, self.device)
-        rc = _pkg.lib().dflash2_adamw(self._table, len(self._table), self.state_bits, self.beta1, self.beta2,
-                                      self.eps, self.step_count + 1, _pkg._p(grad_scale), s)
+        rc = _pkg.lib().dflash2_adamw(self._table, len(self.params), self.state_bits, self.beta1, self.beta2,
+                                      self.eps, self.step_count + 1, _pkg._ptr(grad_scale),
+                                      _pkg._stream(stream, self.device))
         _pkg._check("dflash2_adamw", rc)
         self.step_count += 1
 
