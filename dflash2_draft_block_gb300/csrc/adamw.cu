@@ -1,8 +1,8 @@
 // dflash2_adamw: one AdamW step over many tensors.
 //
-// Per element, each line one or two separately rounded fp32 operations (no fused
-// multiply-add, so a result depends on the formula alone and not on how a compiler
-// contracts it):
+// Per element, in fp32 operations that are rounded one by one (no fused multiply-add, so
+// the moments depend on the formula alone and not on how a compiler contracts it; the
+// division of the update is the fast one, within 2 ulp of an lr-sized term):
 //   g = grad * grad_scale
 //   m = m * beta1 + g * (1 - beta1)
 //   v = v * beta2 + (g * (1 - beta2)) * g
@@ -17,10 +17,16 @@
 // block's largest value is held exactly (to an ulp), so a block whose gradients fade
 // fades with its scale although e4m3's steps are wider than one step's decay.
 //
-// Bound: HBM.  A step reads w, g, m, v and writes w, m, v (and the bf16 copy of a
-// master weight) once: 28 bytes an element with everything in fp32.  One warp owns a
-// block of 256 elements, 8 a lane: the block's maxima are warp shuffles, every load
-// is 16 bytes a lane, and all of a lane's loads are issued before the first use.
+// Bound: HBM.  A step reads w, g, m, v and writes w, m, v (and the bf16 copy of a master
+// weight) once: 28 bytes an element with everything in fp32.  One warp owns a block of 256
+// elements, 8 a lane: the block's maxima are warp shuffles, every load is 16 bytes a lane,
+// and all of a lane's loads are issued before the first use, the gradient scale's among
+// them.  Four warps a CTA: its warps end together, and a smaller CTA gives way sooner (213
+// against 222 us with eight, 8-bit states of 78.8 M bf16 weights with masters: 6.7 TB/s;
+// the exact division instead of the fast one and the scale checked before the loads took
+// 280 us).  Two blocks a warp with the next one's loads in flight need 126 registers and
+// took 303 us.  States in fp32 with bf16 weights, gradients and masters: 42.9 M weights in
+// 175 us, 6.9 TB/s.
 // One launch covers up to kManyTensors tensors: their descriptors travel as the
 // kernel's parameters, so nothing is uploaded and no table of addresses outlives the
 // call; a warp finds its tensor by bisection over the block counts.
@@ -35,7 +41,7 @@ namespace df2 {
 namespace {
 
 constexpr int kBlock = DF2_ADAMW_BLOCK;  // elements a warp owns, and that share a scale
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kFewTensors = 16;
 constexpr int kManyTensors = 320;
 constexpr float kE4m3Max = 448.f;
@@ -137,11 +143,7 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
     const int blk = blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (blk >= a.first[a.count]) return;
-    float gs = 1.f;
-    if (a.grad_scale) {
-        gs = __ldg(a.grad_scale);
-        if (!isfinite(gs)) return;  // no usable gradient: the step is left out
-    }
+    const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.f;
     int lo = 0, hi = a.count;  // first[lo] <= blk < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -198,7 +200,8 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
         }
     }
 
-    float top_m = 0.f, top_s = 0.f;
+    if (!isfinite(gs)) return;  // no usable gradient: the step is left out
+    float top_m = 0.f, top_s = 0.f;  // (elements past the end are zeros all through)
     float root[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -212,8 +215,8 @@ __global__ void __launch_bounds__(kWarps * 32) adamw_kernel(const __grid_constan
         v[k] = __fadd_rn(__fmul_rn(v[k], a.b2), __fmul_rn(__fmul_rn(gk, a.c2), gk));
         root[k] = __fsqrt_rn(v[k]);
         const float den = __fadd_rn(__fmul_rn(root[k], a.inv_bc2), a.eps);
-        w[k] = __fsub_rn(__fmul_rn(w[k], t.keep), __fmul_rn(__fdiv_rn(m[k], den), t.step));
-        if (BITS == 8 && k < left) {
+        w[k] = __fsub_rn(__fmul_rn(w[k], t.keep), __fmul_rn(__fdividef(m[k], den), t.step));
+        if (BITS == 8) {
             top_m = fmaxf(top_m, fabsf(m[k]));
             top_s = fmaxf(top_s, root[k]);
         }

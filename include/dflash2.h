@@ -514,7 +514,8 @@ int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dout_ld, co
  * dflash2_adamw — one AdamW step (decoupled weight decay) over many tensors.
  *
  * No counterpart in the pages, which leave the optimiser open.  For every element of
- * every tensor, in separately rounded fp32 operations, with t = step:
+ * every tensor, in separately rounded fp32 operations (the update's division: 2 ulp), with
+ * t = step:
  *   g = grad * grad_scale                       (grad_scale NULL: 1)
  *   m = beta1 * m + (1 - beta1) * g
  *   v = beta2 * v + (1 - beta2) * g * g
