@@ -131,6 +131,43 @@ def test_shapes(df2, P, K, r, V, dtype):
     near(loss[live], ref["loss"][0][live], ref["loss"][1][live], "selector_ce")
 
 
+@pytest.mark.parametrize("P, K, r, V", [
+    (5003, 16, 256, 9000), (2441, 17, 72, 700), (2500, 8, 136, 500), (3001, 1, 1024, 300), (2600, 128, 8, 3000),
+    (2433, 33, 40, 900), (1300, 40, 256, 2000), (700, 64, 256, 4000), (650, 100, 200, 1000), (400, 64, 512, 5000),
+    (311, 31, 1000, 600), (305, 128, 264, 800), (320, 2, 4096, 200),
+])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_many_rows(df2, P, K, r, V, dtype):
+    """More rows than the GPU holds at once, and candidate lists long enough to be sorted in
+    every size class (up to 16 k, 64 k and more positions, one of several tiles a CTA)."""
+    c = case(P + K, P, K, r, V)
+    live = covered_rows(c)
+    c["G"][~live] = float("nan")
+    got, _ = check(df2, c, live, dtype)
+    again = df2.selector_loss_grad(**c, dtype=dtype)
+    for x, y in zip(got, again):
+        assert torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0))
+    # without the tables nothing is sorted, and the rows run by themselves
+    part = df2.selector_loss_grad(**c, dA=None, dBc=None)
+    for x, y in zip(part[:4], got[:4]):
+        assert torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0))
+
+
+def test_many_rows_masks_and_bad_ids(df2):
+    c = case(21, 3000, 16, 256, 4000, covered=1.0)
+    bad = torch.arange(3000, device="cuda") % 97 == 0
+    c["topk_ids"][bad, 3] = 4000
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    check(df2, c, covered_rows(c) & ~bad, dev_status=st)
+    assert int(st) == df2.DF2_STATUS_ID_OUT_OF_RANGE
+    none = torch.arange(3000, device="cuda") % 89 == 0
+    c["topk_vals"][none] = float("-inf")
+    got = df2.selector_loss_grad(**c)
+    dead = bad | none
+    assert torch.all(got[1][dead] == -1) and torch.all(got[0][dead].isnan()) and torch.all(got[2][dead] == 0)
+    assert torch.all(got[1][~dead] >= 0) and all(torch.all(x.isfinite()) for x in got[2:])
+
+
 @pytest.mark.parametrize("covered", [0.0, 1.0])
 def test_no_row_and_every_row(df2, covered):
     c = case(5, 50, 8, 64, 400, covered)
