@@ -145,6 +145,17 @@ __device__ __forceinline__ Out out_of(const FoldArgs& a, int64_t slice, int gl) 
     return Out{static_cast<char*>(a.out) + c * sz, uint64_t(a.out_ld) * sz, a.D - c, a.scale, a.accumulate};
 }
 
+// Adds to global memory that return nothing (of an atomicAdd on a generic pointer the old
+// value comes back, wanted or not).
+__device__ __forceinline__ void add1(float* p, float x) {
+    asm volatile("red.relaxed.gpu.global.add.f32 [%0], %1;" ::"l"(__cvta_generic_to_global(p)), "f"(x) : "memory");
+}
+__device__ __forceinline__ void add4(float4* p, float4 x) {
+    asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(__cvta_generic_to_global(p)),
+                 "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w)
+                 : "memory");
+}
+
 // A row's columns = scale * f (+ themselves).  Added in fp32 by the memory's own add: a row
 // has one writer, so the result is the one rounded sum, and nobody waits for the old row
 // (the add flushes subnormal operands).
@@ -169,8 +180,8 @@ __device__ __forceinline__ void put_columns(char* p, int64_t left, float scale, 
             x = make_float4(g[0], g[1], g[2], g[3]);
             y = make_float4(g[4], g[5], g[6], g[7]);
             if (accumulate) {
-                atomicAdd(q, x);
-                atomicAdd(q + 1, y);
+                add4(q, x);
+                add4(q + 1, y);
             } else {
                 q[0] = x;
                 q[1] = y;
@@ -193,7 +204,7 @@ __device__ __forceinline__ void put_columns(char* p, int64_t left, float scale, 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             if (i * L >= left) continue;
-            if (accumulate) atomicAdd(q + i * L, g[i]);
+            if (accumulate) add1(q + i * L, g[i]);
             else q[i * L] = g[i];
         }
     }
@@ -397,6 +408,7 @@ __device__ __forceinline__ void fold_chunk(const Plan& p) {
         unsigned live = __ballot_sync(gmask, on) >> (lane & ~(L - 1));
         unsigned begins = __ballot_sync(gmask, gl < n && key != (gl ? before : cur)) >> (lane & ~(L - 1));
         more = __shfl_sync(gmask, key, n - 1, L) != none;
+#pragma unroll 1
         for (int j = 0; j < n; j += kAhead, live >>= kAhead, begins >>= kAhead) {
             Row<SRC16, W, L> r[kAhead];
 #pragma unroll
@@ -559,10 +571,10 @@ __global__ void __launch_bounds__(kThreads) fold_small_kernel(const __grid_const
 int lanes_of(int64_t D) { return D <= 64 ? 8 : 32; }
 int64_t slices_of(int64_t D, int L) { return (D + 8 * L - 1) / (8 * L); }
 
-// Positions a chunk: a power of two that leaves each of 152 SMs 32 warps, within 16 .. 512
+// Positions a chunk: a power of two that leaves each of 152 SMs 32 warps, within 8 .. 512
 // (shorter chunks leave more parts, longer ones fewer warps).
 int chunk_of(int64_t N, int64_t D, int L) {
-    int E = 16;
+    int E = 8;
     while (E < 512 && N * slices_of(D, L) * L > int64_t(E) * 152 * 32 * 32) E *= 2;
     return E;
 }
