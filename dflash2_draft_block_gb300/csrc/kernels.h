@@ -198,6 +198,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream);
 struct ZeroArgs {
     char* p[2];
     int64_t bytes[2];
+    int64_t each, extra;  // the launch's: units a CTA, and CTAs that take one more
 };
 
 // ---- the selector's loss and gradients, row by row (selector_loss.cu); u [P, r] =

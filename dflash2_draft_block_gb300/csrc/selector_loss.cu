@@ -96,7 +96,9 @@ __device__ __forceinline__ void send_zeros(const ZeroArgs& z, float* zeros) {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     if (threadIdx.x) return;
-    for (int64_t u = blockIdx.x * n / gridDim.x, end = (blockIdx.x + 1) * n / gridDim.x; u < end; ++u) {
+    const int64_t b = blockIdx.x;
+    int64_t u = b * z.each + dmin<int64_t>(b, z.extra);
+    for (int64_t end = u + z.each + (b < z.extra); u < end; ++u) {
         const int i = u >= n0;
         const int64_t at = (u - (i ? n0 : 0)) * kZeroBytes;
         bulk_store(z.p[i] + at, zeros, uint32_t(dmin<int64_t>(kZeroBytes, z.bytes[i] - at)));
@@ -158,19 +160,19 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
     uint4 b[KW][CH];
     const int per_round = warps * GROUPS * KW;
     auto first_of = [&](int round) { return round * per_round + (warp * GROUPS + group) * KW; };
+    // (past the last candidate or column some other value is read, and not used)
     auto gather = [&](int round) {
         const int j0 = first_of(round);
         int32_t id[KW];
 #pragma unroll
-        for (int k = 0; k < KW; ++k) id[k] = j0 + k < a.K ? __ldg(ids + j0 + k) : -1;
+        for (int k = 0; k < KW; ++k) id[k] = __ldg(ids + min(j0 + k, a.K - 1));
 #pragma unroll
-        for (int k = 0; k < KW; ++k)
+        for (int c = 0; c < CH; ++c) {
+            const int x = (c * L + gl) * 8;
+            const uint16_t* col8 = a.Bc + (x < a.r ? x : 0);
 #pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int x = (c * L + gl) * 8;
-                b[k][c] = make_uint4(0, 0, 0, 0);
-                if (id[k] >= 0 && x < a.r) b[k][c] = __ldg(reinterpret_cast<const uint4*>(a.Bc + int64_t(id[k]) * a.r + x));
-            }
+            for (int k = 0; k < KW; ++k) b[k][c] = __ldg(reinterpret_cast<const uint4*>(col8 + int64_t(id[k]) * a.r));
+        }
     };
     if (live) {
         gather(0);
@@ -258,10 +260,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
         finish(a);
         return;
     }
-    const float w = a.weights ? __ldg(a.weights + p) : 1.f;
+    const float w = a.weights ? __ldg(a.weights + p) : 1.f, inv = 1.f / sum;
     __syncthreads();  // every warp has its maximum and sum: the scores give way to dscores
     for (int j = threadIdx.x; j < a.K; j += blockDim.x) {
-        const float d = w * (expf(sc[j] - m) / sum - (j == col ? 1.f : 0.f));
+        const float d = w * (expf(sc[j] - m) * inv - (j == col ? 1.f : 0.f));
         sc[j] = d;
         a.ds[p * a.K + j] = d;
     }
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
 }
 
 template <int L, int CH>
-cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
+cudaError_t launch(LossArgs a, int64_t P, cudaStream_t stream) {
     constexpr int per_warp = 32 / L * (16 / CH);
     int warps = 1;
     while (warps < kMaxWarps && warps * per_warp < a.K) warps *= 2;
@@ -337,6 +339,8 @@ cudaError_t launch(const LossArgs& a, int64_t P, cudaStream_t stream) {
     const int64_t zeros = zero_units(a.zero, 0) + zero_units(a.zero, 1);
     const size_t smem = loss_smem(warps, a.K, a.r) + (zeros ? kZeroBytes : 0);
     const int64_t blocks = dmax(P, dmin<int64_t>(zeros, kZeroBlocks));
+    a.zero.each = zeros / blocks;
+    a.zero.extra = zeros % blocks;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(selector_loss_kernel<L, CH>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
