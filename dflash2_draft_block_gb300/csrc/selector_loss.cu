@@ -7,16 +7,19 @@
 //   dG = a * t,  and for the folds into the codebooks' gradients: u (weighted by ds_j, for
 //   dBc[id_j]) and G * t (for dA[pred])
 //
-// One CTA a row, of as many warps as hold the row's K x r bf16 values in 64 registers a
-// lane: a group of L lanes covers r (8 columns a lane and chunk, CH chunks), and a lane
-// keeps KW = 16 / CH candidates.  The values are loaded once, used for the scores and,
-// after the softmax, again for t.  Rows too large for eight warps' registers are walked
-// in rounds and loaded a second time for t.  Scores are summed over a group's lanes by
-// halving: at every step a lane hands half of its candidates to its partner, so KW
-// candidates cost about KW shuffles instead of KW * log2(L).
+// One CTA a row.  A group of L lanes covers r (8 columns a lane and chunk, CH chunks), and a
+// lane keeps KW = 16 / CH candidates in 64 registers.  Where the CTA's warps hold the whole
+// row, its values are loaded once, used for the scores and, after the softmax, again for t;
+// larger rows are walked in rounds and loaded a second time for t.  Scores are summed over
+// a group's lanes by halving: at every step a lane hands half of its candidates to its
+// partner, so KW candidates cost about KW shuffles instead of KW * log2(L).  Products are
+// packed two to an instruction.
 //
-// Bound: gathers from L2 and HBM (K rows of 2 r bytes each); all of a row's loads are in
-// flight at once.
+// Bound: gathers from L2 and HBM (K rows of 2 r bytes each), all of a round's loads in
+// flight at once, and the issue of about a thousand instructions a warp.  16,384 rows of 16
+// at rank 256 take 35 us (134 MB gathered, 3.8 TB/s).  Staging the rows in shared memory
+// ahead of the warps, with both contractions on mma.sync (the vectors in three bf16 parts),
+// took 89 us: its loops issue more than they save and leave eight warps an SM.
 //
 // Gradient tables that are to be written whole are cleared here: every CTA sends its share
 // as bulk copies of zeros before its row, which costs the rows little (they wait for gathers
@@ -333,8 +336,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
 template <int L, int CH>
 cudaError_t launch(LossArgs a, int64_t P, cudaStream_t stream) {
     constexpr int per_warp = 32 / L * (16 / CH);
+    // Many rows: two warps a row at most, so that rows in different phases share an SM, and
+    // the second reads come from L2 (4096 rows of 64 at rank 512: 51 us, with up to four
+    // warps 57, with eight 70).  Few rows: up to eight.
+    const int most = P >= 152 * 4 ? 2 : kMaxWarps;
     int warps = 1;
-    while (warps < kMaxWarps && warps * per_warp < a.K) warps *= 2;
+    while (warps < most && warps * per_warp < a.K) warps *= 2;
     const int rounds = (a.K + warps * per_warp - 1) / (warps * per_warp);
     const int64_t zeros = zero_units(a.zero, 0) + zero_units(a.zero, 1);
     const size_t smem = loss_smem(warps, a.K, a.r) + (zeros ? kZeroBytes : 0);
