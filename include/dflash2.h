@@ -494,8 +494,8 @@ int dflash2_embedding(const void* table, int table_dtype, int64_t V, int64_t D, 
  * The ids are sorted first, stably; a token's rows are summed in fp32 in an order that
  * ids and the sizes alone fix, so equal inputs give equal bits, and the sum is rounded
  * to dtable's dtype once.  accumulate = 0: every row is written, those of absent tokens
- * as zeros; accumulate != 0: the sums are added to dtable, and rows of absent tokens are
- * neither read nor written.  Positions with a negative id have no part (their dout is
+ * as zeros; accumulate != 0: the sums are added to dtable (an fp32 dtable: subnormals count
+ * as zero in that add), and rows of absent tokens are neither read nor written.  Positions with a negative id have no part (their dout is
  * not read); an id >= V sets DF2_STATUS_ID_OUT_OF_RANGE and has none either.
  *
  *   dout   [N, D] dout_dtype, rows dout_ld >= D elements apart
