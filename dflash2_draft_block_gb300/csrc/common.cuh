@@ -52,10 +52,12 @@ __device__ __forceinline__ void unpack8(const uint4& w, float f[8]) {
 }
 
 // 1-D bulk copy shared -> global of `bytes` (a multiple of 16; both addresses 16-byte
-// aligned), in the thread's current bulk group.
+// aligned), in the thread's current bulk group, marked to leave L2 first.
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
-                 "r"(uint32_t(__cvta_generic_to_shared(src))), "r"(bytes)
+    uint64_t policy;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;" ::"l"(dst),
+                 "r"(uint32_t(__cvta_generic_to_shared(src))), "r"(bytes), "l"(policy)
                  : "memory");
 }
 

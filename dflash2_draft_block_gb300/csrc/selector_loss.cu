@@ -21,9 +21,10 @@
 // ahead of the warps, with both contractions on mma.sync (the vectors in three bf16 parts),
 // took 89 us: its loops issue more than they save and leave eight warps an SM.
 //
-// Gradient tables that are to be written whole are cleared here: every CTA sends its share
-// as bulk copies of zeros before its row, which costs the rows little (they wait for gathers
-// from L2, the copies for HBM), and the folds then write the rows of tokens only.
+// Gradient tables that are to be written whole may be cleared here: every CTA sends its
+// share as bulk copies of zeros before its row, and the folds then write the rows of tokens
+// only.  (The copies are marked to leave L2 first: as ordinary writes they drove out the
+// rows that the folds read next.)
 #include "common.cuh"
 #include "kernels.h"
 
