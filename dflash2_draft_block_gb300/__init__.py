@@ -565,6 +565,14 @@ def _scratch(nbytes, workspace, dev, stream):
     return ws, ws.data_ptr(), nbytes
 
 
+def _made(stream, *tensors):
+    """Outputs that a call made: kept from other uses until the kernels of `stream` have
+    written them, as a caller who drops one early could not know to."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _ptr(t):
     return t.data_ptr() if t is not None else 0
 
@@ -584,6 +592,7 @@ def embedding(table, ids, *, scale=1.0, dtype=None, dev_status=None, out=None, s
         if odt is None:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
         out = torch.empty((*ids.shape, D), dtype=dtype, device=dev)
+        _made(stream, out)
     else:
         odt, old = _rows(out, "out", (N, D), dev)
         if dtype is not None and dtype != out.dtype:
@@ -628,6 +637,7 @@ def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=F
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
         out = torch.empty((V, D), dtype=dtype, device=dev)
         odt, old = _DTYPES[dtype], max(D, 1)
+        _made(stream, out)
     else:
         odt, old = _rows(out, "out", (V, D), dev)
     if dev_status is not None:
@@ -685,11 +695,14 @@ def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weig
     e = torch.empty
     if dA is True:
         dA = e((V, r), dtype=dtype, device=dev)
+        _made(stream, dA)
     if dBc is True:
         dBc = e((V, r), dtype=dtype, device=dev)
+        _made(stream, dBc)
     if out is None:
         loss, label = e((P,), dtype=torch.float32, device=dev), e((P,), dtype=torch.int32, device=dev)
         ds, dG = e((P, K), dtype=torch.float32, device=dev), e((P, r), dtype=torch.float32, device=dev)
+        _made(stream, loss, label, ds, dG)
     else:
         loss, label, ds, dG = out
         _out(loss, "loss", torch.float32, P, dev)

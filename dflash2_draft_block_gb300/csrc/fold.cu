@@ -35,10 +35,10 @@ constexpr int kAhead = 4;  // rows in flight a lane
 constexpr int kJoinWarps = 8;
 constexpr int kJoinBlocks = 152 * 4;  // at most: each takes split tokens in turn
 constexpr int kSmall = 512;
-constexpr int kFillRows = 4096;          // rows a fill takes at a time, at most
-constexpr int kZeros = 4096;              // bytes of zeros a fill CTA copies from
-constexpr int64_t kFillBytes = 128 * 1024;  // and the bytes
-constexpr int kFillBlocks = 152;          // CTAs that only fill, the first of a launch
+constexpr int kFillRows = 4096;             // rows a fill takes at a time, at most
+constexpr int64_t kFillBytes = 128 * 1024;  // and their bytes
+constexpr int kFillBlocks = 152;            // CTAs that only fill, the first of a launch
+constexpr int kZeros = 4096;                // bytes of zeros a filling CTA copies from
 
 struct Plan {
     FoldArgs a[kMaxJobs];
@@ -221,7 +221,7 @@ __device__ __noinline__ void put_columns_call(char* p, int64_t left, float scale
 template <bool OUT16, int W, int L>
 __device__ __forceinline__ void put_row(const Out& o, uint32_t row, const float f[8]) {
     const float4 x = make_float4(f[0], f[1], f[2], f[3]), y = make_float4(f[4], f[5], f[6], f[7]);
-    if (W == 8) put_columns<OUT16, W, L>(o.p + row * o.stride, o.left, o.scale, o.accumulate, x, y);
+    if constexpr (W == 8) put_columns<OUT16, W, L>(o.p + row * o.stride, o.left, o.scale, o.accumulate, x, y);
     else put_columns_call<OUT16, W, L>(o.p + row * o.stride, o.left, o.scale, o.accumulate, x, y);
 }
 
@@ -375,8 +375,7 @@ __device__ __forceinline__ void fold_chunk(const Plan& p) {
 
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const uint32_t none = uint32_t(a.V);
-    const uint64_t begin = __ldg(pairs + i);
-    uint32_t cur = uint32_t(begin);
+    uint32_t cur = key_at(pairs, i);
     if (cur == none) return;
     const Out o = out_of<W, L>(a, slice, gl);
     auto leave = [&](bool is_tail) {  // the current token's sums, to its row or to its part

@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const __grid_c
     // let the next kernel start beside this one (one that was launched to allow it)
     asm volatile("griddepcontrol.launch_dependents;");
     cg::cluster_group cluster = cg::this_cluster();
+    // (waited for before the first store into another CTA's shared memory: it must have begun)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int C = int(cluster.num_blocks()), c = int(cluster.block_rank());
     const bool second = int(blockIdx.x) >= C;  // (a parameter indexed by a register is slow to read)
     const SortJob job = second ? args.job[1] : args.job[0];
@@ -185,6 +187,7 @@ __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const __grid_c
             __syncthreads();
             own = tid < bins ? cell[tid * kCellLd].y : 0u;
         }
+        if (pass == 0) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         if (tid < bins)
             for (int o = 0; o < C; ++o) cluster.map_shared_rank(totals, o)[c * bins + tid] = own;
         cluster.sync();

@@ -138,7 +138,8 @@ class AdamW:
 
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None):
         """One step.  grad_scale: an fp32 CUDA scalar the gradients are multiplied by (a NaN
-        or infinite one leaves the tensors and states as they are).  lr: new learning rates."""
+        or infinite one leaves the tensors and states as they are; the step counts all the
+        same, as the host does not wait to see).  lr: new learning rates."""
         if grads is None:
             grads = self.grads if self.grads is not None else [p.grad for p in self.params]
         if grad_scale is not None:
