@@ -186,11 +186,12 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
         f.out = out;
         f.out_bf16 = table_dtype == DF2_DTYPE_BF16;
         f.accumulate = accumulate != 0;
-        // Where the candidates' rows fit in L2 the rows' kernel leaves the memory bus idle and
-        // clears the tables meanwhile (16384 x 16 at rank 256, 78 MB: 124 us, 129 with the
-        // absent rows cleared by the folds); where they come from HBM the folds clear less
-        // (4096 x 64 at rank 512, 155 MB: 161 us, 166 the other way).
-        const bool beside_rows = P > 0 && df2::dmin<int64_t>(P * K, V) * r * 2 <= (int64_t(96) << 20);
+        // The rows' kernel leaves the memory bus idle and can clear a table meanwhile, but
+        // does not know which rows the fold will write again: it clears a table of which
+        // few rows can be written, the folds clear the others.  (16384 x 16 at rank 256: 123
+        // us, 129 with both left to the folds, 125 with both cleared here; 4096 x 64 at rank
+        // 512: 156, 161, 166.)
+        const bool beside_rows = P > 0 && 4 * N <= V;
         f.fill = !f.accumulate && !beside_rows;
         if (!f.accumulate && beside_rows) {
             zero.p[count - 1] = static_cast<char*>(out);

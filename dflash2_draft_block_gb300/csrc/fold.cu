@@ -12,12 +12,13 @@
 // depends on the sorted list alone, so results repeat bit for bit.  Four rows in flight and
 // 96 registers leave five CTAs an SM (eight rows take 122 and leave four).
 //
-// Where asked (fill), the rows of absent tokens become zeros in the same launch: 152 CTAs
+// Where asked (fill), the rows of absent tokens become zeros in the same launch: some CTAs
 // from the start, and the others when their chunks are done, take ranges of rows off a
 // counter, mark those that the sorted list holds, and clear the others, so every row is
-// written once, and the writes run beside the gathers.  (With fill CTAs spread among the
-// others the folds had a third of the SMs' room; with a fixed share each, one CTA an SM wrote
-// 4.1 TB/s.)
+// written once, and the writes run beside the gathers.  16,384 rows of 5,120 into 248,320
+// bf16 rows take 390 us (2.5 GB written, 6.95 TB/s); with a fixed share of the clearing a
+// CTA 514 us at best; with 152 to 608 CTAs that only clear 418 to 409, and the gathers of
+// other lists lose room to them (141 us with 608, 123 with 114, 16,384 rows of 16 at rank 256).
 //
 // Lists of up to kSmall positions are not sorted at all: every position looks for its equals
 // in the list itself, the first of them owns the token (fold_small_kernel).
@@ -37,7 +38,8 @@ constexpr int kJoinBlocks = 152 * 4;  // at most: each takes split tokens in tur
 constexpr int kSmall = 512;
 constexpr int kFillRows = 4096;             // rows a fill takes at a time, at most
 constexpr int64_t kFillBytes = 128 * 1024;  // and their bytes
-constexpr int kFillBlocks = 152;            // CTAs that only fill, the first of a launch
+constexpr int kFillBlocks = 114;            // CTAs that only fill, the first of a launch: at least,
+constexpr int kAllBlocks = 152 * 5;         // and as many as make so many in all
 constexpr int kZeros = 4096;                // bytes of zeros a filling CTA copies from
 
 struct Plan {
@@ -656,7 +658,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
             const int64_t sz = a.out_bf16 ? 2 : 4, row = a.D * sz;
             const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row % 16 == 0 && (a.out_ld * sz) % 16 == 0;
             p.fill_unit[i] = wide ? 16 : int(sz);
-            const int64_t rows = dmin<int64_t>(dmin<int64_t>(kFillRows, kFillBytes / row), a.V / (kFillBlocks * 8));
+            const int64_t rows = dmin<int64_t>(dmin<int64_t>(kFillRows, kFillBytes / row), a.V / (152 * 8));
             p.fill_rows[i] = int(dmax<int64_t>(1, rows));
             fill = (a.V + p.fill_rows[i] - 1) / p.fill_rows[i];
         }
@@ -667,7 +669,7 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
         fills += fill;
     }
     if (fills > INT32_MAX) return cudaErrorInvalidConfiguration;
-    p.fill_blocks = int(small ? fills : dmin<int64_t>(fills, kFillBlocks));
+    p.fill_blocks = int(small ? fills : dmin(fills, dmax<int64_t>(kFillBlocks, kAllBlocks - blocks)));
     blocks += p.fill_blocks;
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
