@@ -52,7 +52,6 @@ struct Plan {
     int fills[kMaxJobs];      // ranges of fill_rows rows
     int fill_blocks;          // CTAs that do nothing else
     int fill_rows[kMaxJobs];
-    int fill_unit[kMaxJobs];  // bytes a store
 };
 
 __device__ __forceinline__ uint32_t key_at(const uint64_t* pairs, int64_t i) {
@@ -284,29 +283,25 @@ __device__ void fill(const Plan& p, int job, int64_t block, uint32_t* held, int6
         }
     }
     __syncthreads();
-    const int sz = a.out_bf16 ? 2 : 4, unit = p.fill_unit[job];
-    const int64_t ld = a.out_ld * sz, per = a.D * sz / unit;
+    // a row a thread: elements up to a 16-byte boundary, a bulk copy of zeros, the rest
+    const int sz = a.out_bf16 ? 2 : 4;
+    const int64_t ld = a.out_ld * sz, bytes = a.D * sz;
     char* out = static_cast<char*>(a.out) + v0 * ld;
-    if (unit == 16) {  // a bulk copy of zeros a row
-        for (int r = tid; r < rows; r += kThreads) {
-            if (held[r >> 5] >> (r & 31) & 1) continue;
-            for (int64_t o = 0; o < per * 16; o += kZeros) bulk_store(out + r * ld + o, zeros, uint32_t(dmin<int64_t>(kZeros, per * 16 - o)));
-        }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        return;
-    }
-    // lanes across a row; several rows a warp where a row has few units
-    int across = 32;
-    while (across > 1 && across / 2 >= per) across /= 2;
-    const int sub = lane & (across - 1), stride = kThreads / across;
-    for (int r = tid / across; r < rows; r += stride) {
+    auto clear = [&](char* q, int64_t n) {
+        for (int64_t o = 0; o < n; o += sz)
+            if (sz == 2) *reinterpret_cast<uint16_t*>(q + o) = 0;
+            else *reinterpret_cast<uint32_t*>(q + o) = 0;
+    };
+    for (int r = tid; r < rows; r += kThreads) {
         if (held[r >> 5] >> (r & 31) & 1) continue;
         char* q = out + r * ld;
-        if (unit == 4)
-            for (int64_t i = sub; i < per; i += across) reinterpret_cast<uint32_t*>(q)[i] = 0;
-        else
-            for (int64_t i = sub; i < per; i += across) reinterpret_cast<uint16_t*>(q)[i] = 0;
+        const int64_t head = dmin<int64_t>(-reinterpret_cast<intptr_t>(q) & 15, bytes), mid = (bytes - head) & ~int64_t(15);
+        clear(q, head);
+        for (int64_t o = 0; o < mid; o += kZeros)
+            bulk_store(q + head + o, zeros, uint32_t(dmin<int64_t>(kZeros, mid - o)));
+        clear(q + head + mid, bytes - head - mid);
     }
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // The CTA's share of all jobs' fills: ranges off the counter while there are any, or the
@@ -656,8 +651,6 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
         int64_t fill = 0;
         if (a.fill) {
             const int64_t sz = a.out_bf16 ? 2 : 4, row = a.D * sz;
-            const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 15) == 0 && row % 16 == 0 && (a.out_ld * sz) % 16 == 0;
-            p.fill_unit[i] = wide ? 16 : int(sz);
             const int64_t rows = dmin<int64_t>(dmin<int64_t>(kFillRows, kFillBytes / row), a.V / (152 * 8));
             p.fill_rows[i] = int(dmax<int64_t>(1, rows));
             fill = (a.V + p.fill_rows[i] - 1) / p.fill_rows[i];
