@@ -19,6 +19,8 @@
 // bf16 rows take 390 us (2.5 GB written, 6.95 TB/s); with a fixed share of the clearing a
 // CTA 514 us at best; with 152 to 608 CTAs that only clear 418 to 409, and the gathers of
 // other lists lose room to them (141 us with 608, 123 with 114, 16,384 rows of 16 at rank 256).
+// Bulk copies clear what lies between a row's 16-byte boundaries, whatever its width: 37 us
+// against 48 with stores an element (6,338 rows of 303 fp32 into 65,371).
 //
 // Lists of up to kSmall positions are not sorted at all: every position looks for its equals
 // in the list itself, the first of them owns the token (fold_small_kernel).
