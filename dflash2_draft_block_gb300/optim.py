@@ -5,7 +5,8 @@
 """
 from __future__ import annotations
 
-from operator import is_
+import ctypes as ct
+from array import array
 
 import torch
 
@@ -17,6 +18,12 @@ ADAMW_BLOCK = 256
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _NAMES = {32: ("exp_avg", "exp_avg_sq"),
           8: ("exp_avg", "exp_avg_rms", "exp_avg_scale", "exp_avg_rms_scale")}
+_FIELDS = ("param", "exp_avg", "exp_avg_2", "exp_avg_scale", "exp_avg_2_scale")  # of params, then _NAMES
+_WORDS = ct.sizeof(_abi.AdamWTensor) // 8  # of 64 bits, in a descriptor
+
+# (a list's worth of one attribute by map() takes half the time of a loop)
+_PTR, _NUMEL, _DENSE, _DEVICE = (getattr(torch.Tensor, k) for k in ("data_ptr", "numel", "is_contiguous", "get_device"))
+_NBYTES, _DTYPE = torch.Tensor.nbytes.__get__, torch.Tensor.dtype.__get__
 
 
 def _each(value, n, name):
@@ -58,6 +65,10 @@ class AdamW:
     state, step     the lists named above and the steps done, as state_dict() gives them;
                     None and 0: zeros
 
+    Every step uses params, grads, master_weights, state, lr, weight_decay and the other
+    attributes as they are then: tensors may move, and be replaced by others of their
+    type and length.  Between steps the handle keeps no gradient that it was not made with.
+
     The states belong to the stream the handle was made on; `step` runs on `stream` (default:
     the current one), and the caller orders the streams where they differ."""
 
@@ -78,15 +89,13 @@ class AdamW:
         if master_weights is True:
             master_weights = [p.detach().to(torch.float32, copy=True) for p in self.params]
         self.master_weights = list(master_weights) if master_weights else None
-        if self.master_weights is not None:
-            self._list(self.master_weights, "master_weights", torch.float32, 1)
         self.state = self._fresh() if state is None else {k: list(state[k]) for k in _NAMES[state_bits]}
-        for name, ts in self.state.items():
-            scale = name.endswith("_scale")
-            held = torch.float8_e4m3fn if state_bits == 8 and not scale else torch.float32
-            self._list(ts, name, held, ADAMW_BLOCK if scale else 1)
+        self._check()
         self.grads = list(grads) if grads is not None else None
-        self._bound = self._ptrs = self._table = None
+        words = array("Q", bytes(8 * _WORDS * max(n, 1)))
+        self._table = (_abi.AdamWTensor * n).from_buffer(words)
+        self._words = {"Q": memoryview(words), "d": memoryview(words).cast("B").cast("d")}
+        self._seen = self._rates = None
 
     def _list(self, ts, name, dtype, per):
         if len(ts) != len(self.params):
@@ -112,29 +121,74 @@ class AdamW:
             state[name] = parts
         return state
 
-    def _bind(self, grads):
-        """The descriptors of a step whose tensors are not those of the last one."""
-        if len(grads) != len(self.params):
-            raise ValueError(f"{len(grads)} gradients for {len(self.params)} parameters")
-        if self.params:
-            _pkg._device(self.params[0])
-        table = (_abi.AdamWTensor * len(self.params))()
-        first, second = _NAMES[self.state_bits][:2]
-        for i, (p, g) in enumerate(zip(self.params, grads)):
-            e = table[i]
-            e.lr, e.weight_decay = self.lr[i], self.weight_decay[i]
-            e.param_dtype = _DTYPES[_tensor(p, f"params[{i}]", _DTYPES, self.state[first][i].numel(), self.device).dtype]
-            if g is None:
-                continue  # n = 0: left out
-            e.grad_dtype = _DTYPES[_tensor(g, f"grads[{i}]", _DTYPES, p.numel(), self.device).dtype]
-            e.param, e.grad, e.n = p.data_ptr(), g.data_ptr(), p.numel()
-            e.exp_avg, e.exp_avg_2 = self.state[first][i].data_ptr(), self.state[second][i].data_ptr()
-            if self.master_weights is not None:
-                e.master = self.master_weights[i].data_ptr()
-            if self.state_bits == 8:
-                e.exp_avg_scale = self.state["exp_avg_scale"][i].data_ptr()
-                e.exp_avg_2_scale = self.state["exp_avg_rms_scale"][i].data_ptr()
-        return table
+    def _check(self):
+        """Parameters, masters and states that fit one another and the device."""
+        for i, p in enumerate(self.params):
+            _tensor(p, f"params[{i}]", _DTYPES, None, self.device)
+        if self.master_weights is not None:
+            self._list(self.master_weights, "master_weights", torch.float32, 1)
+        for name in _NAMES[self.state_bits]:
+            scale = name.endswith("_scale")
+            held = torch.float8_e4m3fn if self.state_bits == 8 and not scale else torch.float32
+            self._list(self.state[name], name, held, ADAMW_BLOCK if scale else 1)
+
+    def _column(self, field, values, code="Q"):
+        """A field of every descriptor."""
+        self._words[code][getattr(_abi.AdamWTensor, field).offset // 8::_WORDS] = array(code, values)
+
+    def _describe(self, grads):
+        """The step's descriptors, from the tensors and rates as they are now.  Every tensor's
+        address and bytes and a gradient's type and layout are read at every step, and nothing
+        is kept but those; where they are what they were, the checks and the columns hold."""
+        params, n = self.params, len(self.params)
+        if len(grads) != n:
+            raise ValueError(f"{len(grads)} gradients for {n} parameters")
+        if n != len(self._table):
+            raise ValueError(f"the handle was made for {len(self._table)} parameters, now there are {n}")
+        if n == 0:
+            return
+        given = grads
+        for g in grads:
+            if g is None:  # its parameter stands in, and its length becomes 0
+                given = [p if g is None else g for p, g in zip(params, grads)]
+                break
+        every = [*given, *params]
+        for name in _NAMES[self.state_bits]:
+            every += self.state[name]
+        if self.master_weights is not None:
+            every += self.master_weights
+        seen = list(map(_PTR, every)), list(map(_NBYTES, every)), list(map(_DTYPE, given)), given is grads
+        if seen != self._seen or given is not grads or not all(map(_DENSE, given)):
+            last, self._seen = self._seen, None
+            if last is None or any(a[n:] != b[n:] for a, b in zip(seen[:2], last)):
+                self._held(seen[0])
+            if list(map(_NUMEL, given)) != self._numels or not all(map(_DENSE, given)) or \
+                    not _DTYPES.keys() >= set(seen[2]) or set(map(_DEVICE, given)) != self._index:
+                for i, (p, g) in enumerate(zip(params, given)):
+                    _tensor(g, f"grads[{i}]", _DTYPES, p.numel(), self.device)
+            self._column("grad", seen[0][:n])
+            self._column("n", [0 if g is None else k for g, k in zip(grads, self._numels)])
+            # and grad_dtype, the other half of the word
+            self._column("param_dtype", [p | _DTYPES[d] << 32 for p, d in zip(self._codes, seen[2])])
+            self._seen = seen
+
+        if (self.lr, self.weight_decay) != self._rates:
+            self.lr, self.weight_decay = _each(self.lr, n, "lr"), _each(self.weight_decay, n, "weight_decay")
+            self._column("lr", self.lr, "d")
+            self._column("weight_decay", self.weight_decay, "d")
+            self._rates = list(self.lr), list(self.weight_decay)
+
+    def _held(self, ptrs):
+        """Checks and columns of the parameters, the states and the masters (ptrs: after the
+        gradients', in this order)."""
+        self._check()
+        n = len(self.params)
+        fields = _FIELDS[:1 + len(_NAMES[self.state_bits])]
+        for i, field in enumerate(fields, 1):
+            self._column(field, ptrs[i * n:(i + 1) * n])
+        self._column("master", ptrs[(1 + len(fields)) * n:] or [0] * n)
+        self._numels, self._codes = [p.numel() for p in self.params], [_DTYPES[p.dtype] for p in self.params]
+        self._index = {p.get_device() for p in self.params}
 
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None):
         """One step.  grad_scale: an fp32 CUDA scalar the gradients are multiplied by (a NaN
@@ -146,14 +200,7 @@ class AdamW:
             _tensor(grad_scale, "grad_scale", (torch.float32,), 1, self.device)
         if lr is not None:
             self.lr = _each(lr, len(self.params), "lr")
-            self._bound = None
-        # the same tensors where they were: the last step's descriptors hold
-        ptrs = [t.data_ptr() for t in self.params] + [0 if g is None else g.data_ptr() for g in grads]
-        if self._bound is None or ptrs != self._ptrs or len(grads) != len(self._bound) or \
-                not all(map(is_, grads, self._bound)):
-            self._bound = None
-            self._table = self._bind(grads)
-            self._ptrs, self._bound = ptrs, list(grads)
+        self._describe(grads)
         if not self.params:
             return
         rc = _pkg.lib().dflash2_adamw(self._table, len(self.params), self.state_bits, self.beta1, self.beta2,

@@ -1,0 +1,48 @@
+"""The AdamW handle on the GPU: states that move between steps."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def df2():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import dflash2_draft_block_gb300 as m
+    m.lib()
+    return m
+
+
+def randn(seed, *shape):
+    return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_that_went_to_the_host_and_back(df2, bits):
+    """Every state, scale and master moved through host memory between two steps, in place and as
+    replaced lists: the same weights as without."""
+    p, q, gs = randn(4, 3000).to(BF), None, [randn(20 + t, 3000) for t in range(6)]
+    q = p.clone()
+    kw = dict(lr=1e-2, state_bits=bits, master_weights=True)
+    stay, move = df2.AdamW([p], **kw), df2.AdamW([q], **kw)
+    for t, g in enumerate(gs):
+        if t in (2, 3):
+            for ts in (*move.state.values(), move.master_weights):
+                for x in ts:
+                    x.data = x.data.cpu()
+            torch.empty(1 << 20, device="cuda").fill_(float("nan"))   # takes what they left
+            for ts in (*move.state.values(), move.master_weights):
+                for x in ts:
+                    x.data = x.data.cuda()
+        if t == 4:
+            move.state = {k: [x.clone() for x in ts] for k, ts in move.state.items()}
+            move.master_weights = [x.clone() for x in move.master_weights]
+        stay.step([g])
+        move.step([g])
+    torch.cuda.synchronize()
+    assert torch.equal(p, q)
+    for k in stay.state:
+        assert torch.equal(stay.state[k][0].view(torch.uint8), move.state[k][0].view(torch.uint8)), k
