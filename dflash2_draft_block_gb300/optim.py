@@ -203,6 +203,7 @@ class AdamW:
         self._describe(grads)
         if not self.params:
             return
+        _pkg._device(self.params[0])
         rc = _pkg.lib().dflash2_adamw(self._table, len(self.params), self.state_bits, self.beta1, self.beta2,
                                       self.eps, self.step_count + 1, _pkg._ptr(grad_scale),
                                       _pkg._stream(stream, self.device))

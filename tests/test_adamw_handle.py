@@ -175,6 +175,24 @@ def test_gradients_and_replaced_states_are_let_go(fake):
     assert ref() is None
 
 
+def test_every_step_asks_for_the_current_device(fake, monkeypatch):
+    """With another device made current between two steps, nothing is launched there."""
+    opt = handle(32)
+    opt.step()
+    opt.step()
+    done = len(fake.calls)
+
+    def other(first, **others):
+        raise ValueError(f"the tensors are on {first.device} but the current CUDA device is another")
+    with monkeypatch.context() as m:
+        m.setattr(df2, "_device", other)
+        with pytest.raises(ValueError):
+            opt.step()
+    assert len(fake.calls) == done and opt.step_count == 2
+    opt.step()
+    assert len(fake.calls) == done + 1
+
+
 def test_no_parameters(fake):
     opt = df2.AdamW([], [])
     opt.step()

@@ -24,7 +24,7 @@ def randn(seed, *shape):
 def test_states_that_went_to_the_host_and_back(df2, bits):
     """Every state, scale and master moved through host memory between two steps, in place and as
     replaced lists: the same weights as without."""
-    p, q, gs = randn(4, 3000).to(BF), None, [randn(20 + t, 3000) for t in range(6)]
+    p, gs = randn(4, 3000).to(BF), [randn(20 + t, 3000) for t in range(6)]
     q = p.clone()
     kw = dict(lr=1e-2, state_bits=bits, master_weights=True)
     stay, move = df2.AdamW([p], **kw), df2.AdamW([q], **kw)
