@@ -75,6 +75,16 @@ def _stream(stream, device):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+def _capturing(stream, device):
+    """Whether what is launched on `stream` (default: the current one) goes into a graph."""
+    if device.type != "cuda":
+        return False
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _need(t, name, dtype, ndim=None):
     if not isinstance(t, torch.Tensor) or not _on_device(t):
         raise TypeError(f"{name} must be a CUDA tensor")

@@ -193,7 +193,10 @@ class AdamW:
     def step(self, grads=None, *, grad_scale=None, lr=None, stream=None):
         """One step.  grad_scale: an fp32 CUDA scalar the gradients are multiplied by (a NaN
         or infinite one leaves the tensors and states as they are; the step counts all the
-        same, as the host does not wait to see).  lr: new learning rates."""
+        same, as the host does not wait to see).  lr: new learning rates.
+
+        The step's number and rates are the host's, so a step is refused while its stream is
+        being captured into a CUDA graph."""
         if grads is None:
             grads = self.grads if self.grads is not None else [p.grad for p in self.params]
         if grad_scale is not None:
@@ -204,6 +207,9 @@ class AdamW:
         if not self.params:
             return
         _pkg._device(self.params[0])
+        if _pkg._capturing(stream, self.device):
+            raise RuntimeError("an AdamW step cannot be captured: its replays would all be this step, with its bias "
+                               "corrections and rates")
         rc = _pkg.lib().dflash2_adamw(self._table, len(self.params), self.state_bits, self.beta1, self.beta2,
                                       self.eps, self.step_count + 1, _pkg._ptr(grad_scale),
                                       _pkg._stream(stream, self.device))

@@ -193,6 +193,18 @@ def test_every_step_asks_for_the_current_device(fake, monkeypatch):
     assert len(fake.calls) == done + 1
 
 
+def test_a_step_is_not_captured(fake, monkeypatch):
+    opt = handle(32)
+    opt.step()
+    with monkeypatch.context() as m:
+        m.setattr(df2, "_capturing", lambda stream, device: True)
+        with pytest.raises(RuntimeError, match="captur"):
+            opt.step()
+    assert len(fake.calls) == 1 and opt.step_count == 1
+    opt.step()
+    assert fake.calls[-1][1] == 2
+
+
 def test_no_parameters(fake):
     opt = df2.AdamW([], [])
     opt.step()

@@ -1,4 +1,4 @@
-"""The AdamW handle on the GPU: states that move between steps."""
+"""The AdamW handle on the GPU: states that move between steps, and steps under capture."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -18,6 +18,24 @@ def df2():
 
 def randn(seed, *shape):
     return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+def test_a_step_is_not_captured(df2):
+    """A replayed step would be the same step for ever: capture is refused, and nothing counts."""
+    p, g = randn(2, 5000), randn(3, 5000)
+    opt = df2.AdamW([p], [g])
+    opt.step()
+    torch.cuda.synchronize()
+    was = p.clone()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="captur"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            opt.step()
+    torch.cuda.synchronize()
+    assert opt.step_count == 1 and torch.equal(p, was)
+    opt.step()
+    torch.cuda.synchronize()
+    assert opt.step_count == 2 and not torch.equal(p, was)
 
 
 @pytest.mark.parametrize("bits", [32, 8])
