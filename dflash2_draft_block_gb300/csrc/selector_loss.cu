@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
         }
     }
     if (threadIdx.x == 0) {  // (before the scores give way below)
-        a.loss[p] = live ? logf(sum) + m - sc[col] : kNan;
+        // (the scores' difference first: next to a large m the logarithm would be rounded away)
+        a.loss[p] = live ? logf(sum) + (m - sc[col]) : kNan;
         a.label[p] = live ? col : -1;
     }
     if (!live) {
