@@ -272,7 +272,8 @@ namespace {
 // The selector's K-way cross-entropy ([PR62] "Selector training objective"): one
 // warp per row.  The lanes stride the row's K scores for its maximum and the first
 // column holding the target, then sum exp(score - maximum); lane 0 writes
-// loss = log(sum) + maximum - score[label].  Rows whose target is not a candidate
+// loss = log(sum) + (maximum - score[label]), the difference first: next to a large
+// maximum the logarithm would be rounded away.  Rows whose target is not a candidate
 // (or is negative) get label -1 and NaN.
 constexpr int kCeWarps = 8;
 
@@ -311,7 +312,7 @@ selector_ce_kernel(const float* __restrict__ scores, const int32_t* __restrict__
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
     if (lane == 0) {
-        loss[p] = logf(sum) + m - __ldg(s + js);
+        loss[p] = logf(sum) + (m - __ldg(s + js));
         if (label_idx) label_idx[p] = js;
     }
 }

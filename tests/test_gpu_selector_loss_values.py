@@ -72,3 +72,13 @@ def test_the_loss_of_scores_far_from_zero(df2, offset, P, K, r):
     if offset == "lowest":
         want = torch.full((P, K), 1.0 / K, device="cuda").scatter_add_(1, col[:, None], torch.full((P, 1), -1.0, device="cuda"))
         assert torch.all((ds - want).abs() <= 8 * U)
+
+
+@pytest.mark.parametrize("offset", OFFSETS)
+@pytest.mark.parametrize("P, K", [(40, 16), (30, 2), (9, 100), (3, 1000)])
+def test_the_forward_call_of_scores_far_from_zero(df2, offset, P, K):
+    c, col = case(P + K, P, K, 8, 1100)
+    s = scores(offset, P, K, torch.Generator(device="cuda").manual_seed(3))
+    loss, label = df2.selector_ce(s, c["topk_ids"], c["targets"], 1100)
+    assert torch.equal(label.long(), col)
+    near_loss(loss, s, col)
