@@ -248,7 +248,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 2) selector_loss_kernel(const 
         for (int j = lane; j < a.K; j += 32) m = fmaxf(m, sc[j]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        live = m != -INFINITY;  // every candidate masked: nothing to learn
+        live = m != -INFINITY;
+        if (!live) {  // every candidate masked, nothing to learn; or NaN, which the maximum leaves out
+            bool nan = false;
+            for (int j = lane; j < a.K; j += 32) nan |= isnan(sc[j]);
+            live = __any_sync(kFull, nan);
+        }
         if (live) {
             for (int j = lane; j < a.K; j += 32) sum += expf(sc[j] - m);
             sum = warp_sum(sum);

@@ -447,6 +447,7 @@ int dflash2_conv_finish_prepare(const void* z, int dtype, int64_t P, int C, int 
  * targets or topk_ids (which sets DF2_STATUS_ID_OUT_OF_RANGE), and one whose scores are
  * all -inf contribute nothing: loss NaN, label_idx -1, dscores and dG zero, and their G,
  * topk_vals and weight are not used.
+ * A NaN among the scores of any other row reaches its loss (label_idx stays) and gradients.
  * dA and dBc are summed in fp32 in an order the ids fix and rounded to table_dtype once;
  * accumulate = 0 writes every row of them, accumulate != 0 adds to the rows of the tokens
  * that occur, as dflash2_embedding_grad does.  NULL leaves one out (a frozen codebook).

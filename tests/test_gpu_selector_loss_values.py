@@ -1,5 +1,5 @@
 """The selector's loss where fp32 could lose it: scores far from zero, rows of nothing but
-the lowest fp32.
+the lowest fp32, NaN.
 
 With G = 0 the scores are topk_vals themselves, so the loss in 64 bits of the same fp32
 scores is what a call should give.  Tolerance, with U = 2^-24 and d_j = s_j - max s: each
@@ -82,3 +82,34 @@ def test_the_forward_call_of_scores_far_from_zero(df2, offset, P, K):
     loss, label = df2.selector_ce(s, c["topk_ids"], c["targets"], 1100)
     assert torch.equal(label.long(), col)
     near_loss(loss, s, col)
+
+
+@pytest.mark.parametrize("P, K, r", [(20, 16, 64), (200, 16, 256), (20, 70, 520)])
+def test_nan_scores_are_no_missing_target(df2, P, K, r):
+    """A covered row whose scores hold a NaN, all of them or one, keeps its label, and its
+    loss and gradients are NaN; the other rows are what they are without it."""
+    V = 4000
+    c, col = case(P, P, K, r, V)
+    c["pred"] = torch.arange(P, device="cuda", dtype=torch.int32) * 3
+    clean = df2.selector_loss_grad(**c)
+    c["G"][0, r - 1] = float("nan")                  # one value reaches every score
+    c["topk_vals"][1] = float("nan")
+    c["topk_vals"][2, K // 2] = float("nan")
+    c["topk_vals"][3] = float("-inf")
+    c["topk_vals"][3, K - 1] = float("nan")
+    c["A"][12, 0] = float("nan")                     # row 4's predecessor
+    c["topk_vals"][5] = float("-inf")                # nothing to learn: dropped, as before
+    loss, label, ds, dG, dA, dBc = df2.selector_loss_grad(**c)
+    nan = torch.arange(P, device="cuda") < 5
+    keep = torch.arange(P, device="cuda") > 5
+    assert torch.equal(label[nan].long(), col[nan]) and int(label[5]) == -1
+    assert torch.all(loss[:6].isnan()) and torch.all(ds[nan].isnan()) and torch.all(dG[nan].isnan())
+    assert torch.all(ds[5] == 0) and torch.all(dG[5] == 0)
+    for got, was in zip((loss, label, ds, dG), clean):
+        assert torch.equal(got[keep], was[keep])
+    at = torch.zeros(V, dtype=torch.bool, device="cuda")
+    at[c["pred"][nan].long()] = True
+    assert torch.all(dA[at].isnan()) and torch.all(dA[~at].isfinite())
+    at = torch.zeros(V, dtype=torch.bool, device="cuda")
+    at[c["topk_ids"][nan].long().view(-1)] = True
+    assert torch.all(dBc[at].isnan()) and torch.all(dBc[~at].isfinite())
