@@ -118,7 +118,7 @@ __device__ __forceinline__ void finish(const LossArgs& a) {
 }
 
 // Shared memory: zeros (where there is something to clear), u [r], scores [K], t parts [warps][r], one word a warp.
-size_t loss_smem(int warps, int K, int r) { return (size_t(warps + 1) * r + K + kMaxWarps) * 4; }
+constexpr size_t loss_smem(int warps, int K, int r) { return (size_t(warps + 1) * r + K + kMaxWarps) * 4; }
 
 // L lanes a group, CH chunks of 8 columns a lane (CH > 1 only with L = 32).
 template <int L, int CH>
@@ -356,8 +356,11 @@ cudaError_t launch(LossArgs a, int64_t P, cudaStream_t stream) {
     a.zero.each = zeros / blocks;
     a.zero.extra = zeros % blocks;
     if (smem > 48 * 1024) {
+        // what the largest call of this kernel needs, whichever call asks: the allowance is the
+        // kernel's, and another host thread may launch it with more meanwhile
+        constexpr size_t most = loss_smem(kMaxWarps, DF2_MAX_TOPK, 8 * L * CH) + kZeroBytes;
         const cudaError_t e = cudaFuncSetAttribute(selector_loss_kernel<L, CH>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};

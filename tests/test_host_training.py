@@ -1,0 +1,149 @@
+"""Host code of the training calls, compiled on the CPU from its own source text (taken out
+of the .cu files by brace matching) against stand-ins for the CUDA runtime that record what
+they are asked.
+
+- `selector_loss_launch`: the shared memory a kernel is allowed is the same whichever call
+  asks for it, and covers every call of that kernel.  (The allowance belongs to the kernel,
+  not to the call: were it a call's own, one host thread could lower it between another's
+  asking and launching.)
+"""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dflash2_draft_block_gb300", "csrc")
+
+
+def _read(name):
+    with open(os.path.join(CSRC, name)) as f:
+        return f.read()
+
+
+def _block(text, start):
+    """From `start` (which must occur once) through its balanced closing brace and a ';'."""
+    assert text.count(start) == 1, start
+    i = text.index(start)
+    depth = 0
+    for k in range(text.index("{", i), len(text)):
+        depth += (text[k] == "{") - (text[k] == "}")
+        if text[k] == "}" and depth == 0:
+            return text[i:k + 1] + (";" if text[k + 1:k + 2] == ";" else "")
+    raise AssertionError("unbalanced braces after " + start)
+
+
+def _line(text, start):
+    assert text.count(start) == 1, start
+    i = text.index(start)
+    return text[i:text.index("\n", i)]
+
+
+STUBS = r"""
+#include <climits>
+#include <cstddef>
+#include <cstdint>
+#include <cstdlib>
+#include <map>
+#define __host__
+#define __device__
+#define __forceinline__ inline
+#define DF2_MAX_TOPK 1024
+#define DF2_MAX_RANK 4096
+typedef int cudaError_t;
+typedef void* cudaStream_t;
+enum { cudaSuccess = 0, cudaErrorInvalidValue = 1 };
+enum { cudaFuncAttributeMaxDynamicSharedMemorySize = 8, cudaFuncAttributeNonPortableClusterSizeAllowed = 14 };
+enum { cudaLaunchAttributeProgrammaticStreamSerialization = 6, cudaLaunchAttributeClusterDimension = 4 };
+struct dim3 { unsigned x, y, z; explicit dim3(unsigned a = 1) : x(a), y(1), z(1) {} };
+struct cudaLaunchAttribute {
+    int id;
+    struct { int programmaticStreamSerializationAllowed; dim3 clusterDim; } val;
+};
+struct cudaLaunchConfig_t {
+    dim3 gridDim, blockDim;
+    size_t dynamicSmemBytes = 0;
+    cudaStream_t stream = nullptr;
+    cudaLaunchAttribute* attrs = nullptr;
+    int numAttrs = 0;
+};
+template <class T> T dmin(T a, T b) { return a < b ? a : b; }
+template <class T> T dmax(T a, T b) { return a < b ? b : a; }
+void note_launch() {}
+// the kernel last asked for or launched, and with how much
+const void* g_kernel;
+long long g_allowed, g_used;
+template <class K> cudaError_t cudaFuncSetAttribute(K* k, int which, int value) {
+    g_kernel = reinterpret_cast<const void*>(k);
+    if (which == cudaFuncAttributeMaxDynamicSharedMemorySize) g_allowed = value;
+    return cudaSuccess;
+}
+template <class K, class... A> cudaError_t cudaLaunchKernelEx(const cudaLaunchConfig_t* c, K* k, A&&...) {
+    g_kernel = reinterpret_cast<const void*>(k);
+    g_used = (long long)c->dynamicSmemBytes;
+    return cudaSuccess;
+}
+"""
+
+
+def _loss_source():
+    loss, kernels = _read("selector_loss.cu"), _read("kernels.h")
+    return "\n".join([
+        _block(kernels, "struct ZeroArgs {"),
+        _line(loss, "constexpr int kMaxWarps"),
+        _block(loss, "struct LossArgs {"),
+        _line(loss, "constexpr int kZeroBytes"),
+        _line(loss, "constexpr int kZeroBlocks"),
+        _block(loss, "__host__ __device__ __forceinline__ int64_t zero_units("),
+        _line(loss, "constexpr size_t loss_smem("),
+        "template <int L, int CH> void selector_loss_kernel(const LossArgs, int) { g_used += L * 100 + CH; }",
+        "template <int L, int CH>\n" + _block(loss, "cudaError_t launch(LossArgs a, int64_t P, cudaStream_t stream) {"),
+        _block(loss, "cudaError_t selector_loss_launch("),
+        r"""
+extern "C" int loss_smem_of(int64_t P, int K, int r, int64_t cleared, long long* kernel, long long* allowed, long long* used) {
+    ZeroArgs z{};
+    z.bytes[0] = cleared;
+    g_kernel = nullptr;
+    g_allowed = -1;
+    const int rc = selector_loss_launch(nullptr, nullptr, P, nullptr, nullptr, nullptr, nullptr, nullptr, 1 << 20, K, r, nullptr,
+                                        nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, z, nullptr, false, nullptr);
+    *kernel = (long long)(intptr_t)g_kernel;
+    *allowed = g_allowed;
+    *used = g_used;
+    return rc;
+}
+"""])
+
+
+@pytest.fixture(scope="module")
+def host(tmp_path_factory):
+    cxx = shutil.which("g++")
+    if not cxx:
+        pytest.skip("no g++")
+    d = tmp_path_factory.mktemp("host_training")
+    src, lib = d / "host.cpp", d / "host.so"
+    src.write_text(STUBS + _loss_source())
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-o", str(lib), str(src)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    return ctypes.CDLL(str(lib))
+
+
+def test_a_kernel_s_shared_memory_does_not_depend_on_the_call(host):
+    allowances, largest = {}, {}
+    k, a, u = (ctypes.c_longlong() for _ in range(3))
+    for r in (8, 32, 40, 64, 72, 128, 136, 256, 264, 512, 520, 1024, 1032, 1536, 2048, 2056, 2064, 3000 // 8 * 8, 4088, 4096):
+        for K in (1, 7, 16, 33, 64, 129, 500, 1024):
+            for P in (1, 40, 607, 608, 5000):
+                for cleared in (0, 1 << 20):
+                    assert host.loss_smem_of(ctypes.c_int64(P), K, r, ctypes.c_int64(cleared), ctypes.byref(k),
+                                             ctypes.byref(a), ctypes.byref(u)) == 0
+                    largest[k.value] = max(largest.get(k.value, 0), u.value)
+                    if a.value >= 0:
+                        allowances.setdefault(k.value, set()).add(a.value)
+                    else:
+                        assert u.value <= 48 * 1024       # what a kernel may use unasked
+    assert allowances and len(largest) == 8
+    for kernel, values in allowances.items():
+        assert len(values) == 1, f"{len(values)} allowances, {min(values)} .. {max(values)}"
+        assert largest[kernel] <= max(values) <= 227 * 1024
