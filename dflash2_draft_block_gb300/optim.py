@@ -54,7 +54,8 @@ class AdamW:
     """AdamW (decoupled weight decay) over `params`, CUDA tensors in bf16 or fp32.
 
     grads           one tensor a parameter, read at every step; None: each step's `grads`,
-                    or the parameters' .grad (a parameter without one is left out)
+                    or the parameters' .grad.  A parameter without one is left out, and the step
+                    is none of its own: its bias corrections count the steps it took
     lr, weight_decay   numbers, or one a parameter
     state_bits      32: exp_avg and exp_avg_sq in fp32.  8: exp_avg and exp_avg_rms, the
                     root of the second moment, as torch.float8_e4m3fn in units of one fp32
@@ -62,8 +63,8 @@ class AdamW:
                     stands for value[i].float() * scale[i // 256]
     master_weights  True: an fp32 copy of every parameter is kept, updated and rounded into
                     it; or the list of those copies
-    state, step     the lists named above and the steps done, as state_dict() gives them;
-                    None and 0: zeros
+    state, step     the lists named above and the steps done (one number, or one a
+                    parameter), as state_dict() gives them; None and 0: zeros
 
     Every step uses params, grads, master_weights, state, lr, weight_decay and the other
     attributes as they are then: tensors may move, and be replaced by others of their
@@ -78,7 +79,13 @@ class AdamW:
             raise ValueError(f"state_bits must be 32 or 8, got {state_bits}")
         self.params = list(params)
         n = len(self.params)
-        self.state_bits, self.step_count, self.eps = state_bits, int(step), float(eps)
+        self.state_bits, self.eps = state_bits, float(eps)
+        steps = [int(t) for t in step] if isinstance(step, (list, tuple)) else [int(step)] * n
+        if len(steps) != n:
+            raise ValueError(f"step must be one number or {n} of them, got {len(steps)}")
+        self.step_count = max(steps, default=0)
+        # how many of them each parameter was left out of (None: none of any)
+        self._late = [self.step_count - t for t in steps] if len(set(steps)) > 1 else None
         self.beta1, self.beta2 = (float(b) for b in betas)
         self.lr, self.weight_decay = _each(lr, n, "lr"), _each(weight_decay, n, "weight_decay")
         self.device = self.params[0].device if n else None
@@ -139,14 +146,15 @@ class AdamW:
     def _describe(self, grads):
         """The step's descriptors, from the tensors and rates as they are now.  Every tensor's
         address and bytes and a gradient's type and layout are read at every step, and nothing
-        is kept but those; where they are what they were, the checks and the columns hold."""
+        is kept but those; where they are what they were, the checks and the columns hold.
+        Returns whether every parameter has a gradient."""
         params, n = self.params, len(self.params)
         if len(grads) != n:
             raise ValueError(f"{len(grads)} gradients for {n} parameters")
         if n != len(self._table):
             raise ValueError(f"the handle was made for {len(self._table)} parameters, now there are {n}")
         if n == 0:
-            return
+            return True
         given = grads
         for g in grads:
             if g is None:  # its parameter stands in, and its length becomes 0
@@ -177,6 +185,7 @@ class AdamW:
             self._column("lr", self.lr, "d")
             self._column("weight_decay", self.weight_decay, "d")
             self._rates = list(self.lr), list(self.weight_decay)
+        return given is grads
 
     def _held(self, ptrs):
         """Checks and columns of the parameters, the states and the masters (ptrs: after the
@@ -203,19 +212,31 @@ class AdamW:
             _tensor(grad_scale, "grad_scale", (torch.float32,), 1, self.device)
         if lr is not None:
             self.lr = _each(lr, len(self.params), "lr")
-        self._describe(grads)
+        whole = self._describe(grads)
         if not self.params:
             return
         _pkg._device(self.params[0])
         if _pkg._capturing(stream, self.device):
             raise RuntimeError("an AdamW step cannot be captured: its replays would all be this step, with its bias "
                                "corrections and rates")
-        rc = _pkg.lib().dflash2_adamw(self._table, len(self.params), self.state_bits, self.beta1, self.beta2,
-                                      self.eps, self.step_count + 1, _pkg._ptr(grad_scale),
-                                      _pkg._stream(stream, self.device))
-        _pkg._check("dflash2_adamw", rc)
+        call = (self.state_bits, self.beta1, self.beta2, self.eps)
+        on = (_pkg._ptr(grad_scale), _pkg._stream(stream, self.device))
+        late = self._late
+        groups = (0,) if late is None else {k for k, g in zip(late, grads) if g is not None}
+        for group in groups:  # of parameters at the same step of their own
+            table = self._table
+            if len(groups) > 1:
+                table = type(table).from_buffer_copy(table)
+                for e, k in zip(table, late):
+                    e.n = e.n if k == group else 0
+            rc = _pkg.lib().dflash2_adamw(table, len(table), *call, self.step_count + 1 - group, *on)
+            _pkg._check("dflash2_adamw", rc)
         self.step_count += 1
+        if not whole:
+            self._late = [k + (g is None) for k, g in zip(late or [0] * len(grads), grads)]
 
     def state_dict(self):
-        """The states (not copies), the master weights and the steps done."""
-        return {"state": self.state, "step": self.step_count, "master_weights": self.master_weights}
+        """The states (not copies), the master weights and the steps done (a list of each
+        parameter's, once one was left out)."""
+        steps = self.step_count if self._late is None else [self.step_count - k for k in self._late]
+        return {"state": self.state, "step": steps, "master_weights": self.master_weights}

@@ -205,6 +205,36 @@ def test_a_step_is_not_captured(fake, monkeypatch):
     assert fake.calls[-1][1] == 2
 
 
+def took(call):
+    table, step = call
+    return step, [i for i, e in enumerate(table) if e.n]
+
+
+def test_a_parameter_counts_its_own_steps(fake):
+    opt = df2.AdamW([zeros(5), zeros(6), zeros(7)])
+    g = [zeros(5), zeros(6), zeros(7)]
+    for have, want in (([1, 0, 1], [(1, [0, 2])]), ([1, 0, 1], [(2, [0, 2])]), ([1, 1, 0], [(3, [0]), (1, [1])]),
+                       ([0, 1, 0], [(2, [1])]), ([0, 0, 0], []), ([1, 1, 1], [(4, [0]), (3, [1, 2])])):
+        done = len(fake.calls)
+        opt.step([x if on else None for x, on in zip(g, have)])
+        got = fake.calls[done:]
+        assert sorted(map(took, got)) == sorted(want)
+        for table, _ in got:
+            for e, x in zip(table, g):
+                assert e.n in (0, x.numel()) and (e.n == 0 or e.grad == x.data_ptr())
+    assert opt.step_count == 6
+    saved = opt.state_dict()
+    assert saved["step"] == [4, 3, 3]
+    again = df2.AdamW(opt.params, **saved)
+    again.step(g)
+    assert sorted(map(took, fake.calls[-2:])) == [(4, [1, 2]), (5, [0])]
+    assert df2.AdamW(opt.params, step=7).state_dict()["step"] == 7
+    assert df2.AdamW(opt.params, step=[7, 7, 7]).state_dict()["step"] == 7
+    for bad in ([1, 2], [1, 2, 3, 4]):
+        with pytest.raises(ValueError):
+            df2.AdamW(opt.params, step=bad)
+
+
 def test_no_parameters(fake):
     opt = df2.AdamW([], [])
     opt.step()

@@ -1,4 +1,5 @@
-"""The AdamW handle on the GPU: states that move between steps, and steps under capture."""
+"""The AdamW handle on the GPU: states that move between steps, steps under capture, and
+parameters whose gradients come late."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -18,6 +19,28 @@ def df2():
 
 def randn(seed, *shape):
     return torch.randn(*shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("first", [2, 7])
+def test_a_late_gradient_starts_at_step_one(df2, bits, first):
+    """A parameter counts its own steps: one whose gradient comes at step `first` moves as in an
+    optimiser of its own, also after the states went through state_dict()."""
+    p, q = randn(0, 1000), randn(1, 700)
+    p1, q1 = p.clone(), q.clone()
+    kw = dict(lr=1e-2, weight_decay=0.1, state_bits=bits)
+    both, a, b = df2.AdamW([p, q], **kw), df2.AdamW([p1], **kw), df2.AdamW([q1], **kw)
+    for t in range(1, 12):
+        gp, gq = randn(10 + t, 1000), randn(50 + t, 700)
+        both.step([gp, gq if t >= first else None])
+        a.step([gp])
+        if t >= first:
+            b.step([gq])
+        if t == first + 2:
+            both = df2.AdamW([p, q], **kw, **both.state_dict())
+    torch.cuda.synchronize()
+    assert torch.equal(p, p1) and torch.equal(q, q1)
+    assert both.step_count == 11
 
 
 def test_a_step_is_not_captured(df2):
