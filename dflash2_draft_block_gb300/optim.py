@@ -9,6 +9,7 @@ import ctypes as ct
 from array import array
 
 import torch
+from torch.autograd.graph import increment_version
 
 import dflash2_draft_block_gb300 as _pkg
 
@@ -231,6 +232,8 @@ class AdamW:
                     e.n = e.n if k == group else 0
             rc = _pkg.lib().dflash2_adamw(table, len(table), *call, self.step_count + 1 - group, *on)
             _pkg._check("dflash2_adamw", rc)
+        # written behind autograd's back: a backward through weights saved before must notice
+        increment_version(self.params if whole else [p for p, g in zip(self.params, grads) if g is not None])
         self.step_count += 1
         if not whole:
             self._late = [k + (g is None) for k, g in zip(late or [0] * len(grads), grads)]

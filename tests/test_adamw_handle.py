@@ -235,6 +235,24 @@ def test_a_parameter_counts_its_own_steps(fake):
             df2.AdamW(opt.params, step=bad)
 
 
+def test_autograd_notices_a_step(fake):
+    """A backward through weights that were saved before a step and stepped since is refused, as
+    after any write in place; one through a parameter that was left out is not."""
+    p, q = (torch.ones(4, requires_grad=True) for _ in range(2))
+    opt = df2.AdamW([p, q], master_weights=True)
+    for t, change in ((p, False), (q, True)):
+        y = (t * t).sum()
+        opt.step([None, zeros(4)])
+        if change:
+            with pytest.raises(RuntimeError, match="inplace"):
+                y.backward()
+        else:
+            y.backward()
+    with torch.inference_mode():
+        w = torch.ones(4)
+    df2.AdamW([w], [zeros(4)]).step()                 # (keeps no version)
+
+
 def test_no_parameters(fake):
     opt = df2.AdamW([], [])
     opt.step()
