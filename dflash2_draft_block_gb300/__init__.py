@@ -561,26 +561,35 @@ def _rows(t, name, shape=None, dev=None):
     return dt, ld
 
 
+def _empty(shape, dtype, dev, stream):
+    """Memory for a call to write, of its stream's own: what the current stream's allocations
+    left free may have work queued there, which another stream does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
 def _scratch(nbytes, workspace, dev, stream):
-    """The caller's workspace, or one of this call's own, which the allocator keeps from
-    other uses until the kernels of `stream` have read it: (tensor, address, bytes)."""
+    """The caller's workspace, or one of this call's own, free for the next call of the
+    stream: (tensor, address, bytes)."""
     if workspace is not None:
         ws = _workspace(nbytes, workspace, dev)
         return ws, ws.data_ptr(), _nbytes(ws)
     if nbytes == 0:
         return None, 0, 0
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)
+    ws = _empty(nbytes, torch.uint8, dev, stream)
     return ws, ws.data_ptr(), nbytes
 
 
-def _made(stream, *tensors):
-    """Outputs that a call made: kept from other uses until the kernels of `stream` have
-    written them, as a caller who drops one early could not know to."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def _made(shape, dtype, dev, stream):
+    """An output that the call makes: kept from other uses until the work of the current stream,
+    where the caller goes on with it, is done, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    t = _empty(shape, dtype, dev, stream)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _ptr(t):
@@ -601,8 +610,7 @@ def embedding(table, ids, *, scale=1.0, dtype=None, dev_status=None, out=None, s
         odt, old = _DTYPES.get(dtype), D
         if odt is None:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        out = torch.empty((*ids.shape, D), dtype=dtype, device=dev)
-        _made(stream, out)
+        out = _made((*ids.shape, D), dtype, dev, stream)
     else:
         odt, old = _rows(out, "out", (N, D), dev)
         if dtype is not None and dtype != out.dtype:
@@ -645,9 +653,8 @@ def embedding_grad(dout, ids, V, *, scale=1.0, dtype=torch.float32, accumulate=F
             raise ValueError("accumulate adds to out: out must be given")
         if dtype not in _DTYPES:
             raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        out = torch.empty((V, D), dtype=dtype, device=dev)
+        out = _made((V, D), dtype, dev, stream)
         odt, old = _DTYPES[dtype], max(D, 1)
-        _made(stream, out)
     else:
         odt, old = _rows(out, "out", (V, D), dev)
     if dev_status is not None:
@@ -702,17 +709,13 @@ def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weig
     for name, t in (("dA", dA), ("dBc", dBc)):
         if t is not None and t is not True:
             _out(t, name, dtype, V * r, dev)
-    e = torch.empty
     if dA is True:
-        dA = e((V, r), dtype=dtype, device=dev)
-        _made(stream, dA)
+        dA = _made((V, r), dtype, dev, stream)
     if dBc is True:
-        dBc = e((V, r), dtype=dtype, device=dev)
-        _made(stream, dBc)
+        dBc = _made((V, r), dtype, dev, stream)
     if out is None:
-        loss, label = e((P,), dtype=torch.float32, device=dev), e((P,), dtype=torch.int32, device=dev)
-        ds, dG = e((P, K), dtype=torch.float32, device=dev), e((P, r), dtype=torch.float32, device=dev)
-        _made(stream, loss, label, ds, dG)
+        loss, label = _made((P,), torch.float32, dev, stream), _made((P,), torch.int32, dev, stream)
+        ds, dG = _made((P, K), torch.float32, dev, stream), _made((P, r), torch.float32, dev, stream)
     else:
         loss, label, ds, dG = out
         _out(loss, "loss", torch.float32, P, dev)
