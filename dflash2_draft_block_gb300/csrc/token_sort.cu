@@ -21,8 +21,7 @@
 // step, by nine votes 36: both queue in one unit; the masks go through shared memory.
 #include <cooperative_groups.h>
 
-#include <mutex>
-#include <unordered_map>
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -242,21 +241,17 @@ __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const __grid_c
     }
 }
 
+constexpr int kMaxDevices = 64;  // whose answers are kept
+
 // 16 CTAs where the device can place such a cluster, else 8 (every device can); asked once
-// a device.
+// a device.  (Threads that ask at the same time set and store the same.)
 template <int ITEMS>
 cudaError_t largest_cluster(cudaLaunchConfig_t* cfg, int* most) {
-    static std::mutex mu;
-    static std::unordered_map<int, int> known;
+    static std::atomic<int> known[kMaxDevices];  // 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto it = known.find(dev);
-    if (it != known.end()) {
-        *most = it->second;
-        return cudaSuccess;
-    }
+    if (dev < kMaxDevices && (*most = known[dev].load(std::memory_order_acquire)) != 0) return cudaSuccess;
     e = cudaFuncSetAttribute(token_sort_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(sort_smem<ITEMS>(kMaxBins)));
     if (e == cudaSuccess)
@@ -269,7 +264,8 @@ cudaError_t largest_cluster(cudaLaunchConfig_t* cfg, int* most) {
     int n = 0;
     e = cudaOccupancyMaxActiveClusters(&n, token_sort_kernel<ITEMS>, &probe);
     if (e != cudaSuccess) return e;
-    *most = known[dev] = n > 0 ? kMaxCluster : 8;
+    *most = n > 0 ? kMaxCluster : 8;
+    if (dev < kMaxDevices) known[dev].store(*most, std::memory_order_release);
     return cudaSuccess;
 }
 

@@ -6,6 +6,9 @@ they are asked.
   asks for it, and covers every call of that kernel.  (The allowance belongs to the kernel,
   not to the call: were it a call's own, one host thread could lower it between another's
   asking and launching.)
+- `largest_cluster` of the sort: asked once a device, of each device for itself, and
+  without memory from the C++ heap, whose exhaustion would leave the C entry as an
+  exception.
 """
 import ctypes
 import os
@@ -41,11 +44,14 @@ def _line(text, start):
 
 
 STUBS = r"""
+#include <atomic>
 #include <climits>
 #include <cstddef>
 #include <cstdint>
 #include <cstdlib>
-#include <map>
+#include <mutex>
+#include <new>
+#include <unordered_map>
 #define __host__
 #define __device__
 #define __forceinline__ inline
@@ -71,6 +77,15 @@ struct cudaLaunchConfig_t {
 template <class T> T dmin(T a, T b) { return a < b ? a : b; }
 template <class T> T dmax(T a, T b) { return a < b ? b : a; }
 void note_launch() {}
+// memory runs out where a test says so; the device, and how many large clusters fit on it
+bool g_no_memory;
+int g_device, g_fit, g_asked;
+cudaError_t cudaGetDevice(int* d) { *d = g_device; return cudaSuccess; }
+template <class K> cudaError_t cudaOccupancyMaxActiveClusters(int* n, K*, const cudaLaunchConfig_t*) {
+    ++g_asked;
+    *n = g_fit;
+    return cudaSuccess;
+}
 // the kernel last asked for or launched, and with how much
 const void* g_kernel;
 long long g_allowed, g_used;
@@ -116,6 +131,42 @@ extern "C" int loss_smem_of(int64_t P, int K, int r, int64_t cleared, long long*
 """])
 
 
+def _sort_source():
+    sort = _read("token_sort.cu")
+    return "\n".join([
+        "void* operator new(size_t n) { if (g_no_memory) throw std::bad_alloc(); return malloc(n ? n : 1); }",
+        "void operator delete(void* p) noexcept { free(p); }",
+        "void operator delete(void* p, size_t) noexcept { free(p); }",
+        "struct SortArgs {};",
+        "template <int ITEMS> void token_sort_kernel(const SortArgs) {}",
+        "template <int ITEMS> size_t sort_smem(int bins) { return bins * ITEMS; }",
+        _line(sort, "constexpr int kMaxCluster"),
+        _line(sort, "constexpr int kMaxDigitBits"),
+        _line(sort, "constexpr int kMaxBins"),
+        "".join(_line(sort, k) + "\n" for k in ("constexpr int kMaxDevices",) if k in sort),
+        "template <int ITEMS>\n" + _block(sort, "cudaError_t largest_cluster(cudaLaunchConfig_t* cfg, int* most) {"),
+        r"""
+extern "C" int cluster_of(int device, int fit, int no_memory, int* most, int* asked) {
+    cudaLaunchAttribute attr[1];
+    cudaLaunchConfig_t cfg;
+    cfg.attrs = attr;
+    g_device = device;
+    g_fit = fit;
+    g_asked = 0;
+    g_no_memory = no_memory != 0;
+    int rc;
+    try {
+        rc = largest_cluster<2>(&cfg, most);
+    } catch (...) {
+        rc = -1;
+    }
+    g_no_memory = false;
+    *asked = g_asked;
+    return rc;
+}
+"""])
+
+
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
     cxx = shutil.which("g++")
@@ -123,8 +174,8 @@ def host(tmp_path_factory):
         pytest.skip("no g++")
     d = tmp_path_factory.mktemp("host_training")
     src, lib = d / "host.cpp", d / "host.so"
-    src.write_text(STUBS + _loss_source())
-    r = subprocess.run([cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-o", str(lib), str(src)], capture_output=True, text=True)
+    src.write_text(STUBS + _loss_source() + _sort_source())
+    r = subprocess.run([cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-o", str(lib), str(src)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     return ctypes.CDLL(str(lib))
 
@@ -147,3 +198,18 @@ def test_a_kernel_s_shared_memory_does_not_depend_on_the_call(host):
     for kernel, values in allowances.items():
         assert len(values) == 1, f"{len(values)} allowances, {min(values)} .. {max(values)}"
         assert largest[kernel] <= max(values) <= 227 * 1024
+
+
+def test_the_largest_cluster_of_each_device(host):
+    most, asked = ctypes.c_int(), ctypes.c_int()
+
+    def ask(device, fit, no_memory=0):
+        assert host.cluster_of(device, fit, no_memory, ctypes.byref(most), ctypes.byref(asked)) == 0
+        return most.value, asked.value
+
+    assert ask(0, 3, no_memory=1) == (16, 1)
+    assert ask(0, 0) == (16, 0)                  # known
+    assert ask(5, 0, no_memory=1) == (8, 1)      # no such cluster fits: the portable size
+    assert ask(5, 0) == (8, 0) and ask(0, 0) == (16, 0)
+    for device in (63, 64, 1000):                # past any table of devices as well
+        assert ask(device, 2, no_memory=1)[0] == 16
