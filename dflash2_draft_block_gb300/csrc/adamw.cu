@@ -355,11 +355,18 @@ DF2_API int dflash2_adamw(const dflash2_adamw_tensor* tensors, int count, int st
     if (!df2::fraction(beta1) || !df2::fraction(beta2) || !df2::finite_nonneg(eps)) return DF2_ERR_INVALID_ARGUMENT;
     if (count > 0 && !tensors) return DF2_ERR_INVALID_ARGUMENT;
     if (!df2::aligned(grad_scale, 4)) return DF2_ERR_UNSUPPORTED;
+    bool any = false;
     for (int i = 0; i < count; ++i) {
         const int rc = df2::check_tensor(tensors[i], state_bits);
         if (rc != DF2_OK) return rc;
+        any |= tensors[i].n > 0;
     }
+    if (!any) return DF2_OK;
     const df2::Hyper h{beta1, beta2, eps, step, grad_scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // the step's number and rates are arguments: a graph would repeat this one step
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &capture) != cudaSuccess) return DF2_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return DF2_ERR_UNSUPPORTED;
     return state_bits == 8 ? df2::launch_all<8>(tensors, count, h, st) : df2::launch_all<32>(tensors, count, h, st);
 }

@@ -16,6 +16,7 @@ import dflash2_draft_block_gb300 as _pkg
 from . import _abi
 
 ADAMW_BLOCK = 256
+_UNSUPPORTED = 2  # DF2_ERR_UNSUPPORTED
 _DTYPES = {torch.bfloat16: 0, torch.float32: 1}
 _NAMES = {32: ("exp_avg", "exp_avg_sq"),
           8: ("exp_avg", "exp_avg_rms", "exp_avg_scale", "exp_avg_rms_scale")}
@@ -217,11 +218,8 @@ class AdamW:
         if not self.params:
             return
         _pkg._device(self.params[0])
-        if _pkg._capturing(stream, self.device):
-            raise RuntimeError("an AdamW step cannot be captured: its replays would all be this step, with its bias "
-                               "corrections and rates")
-        call = (self.state_bits, self.beta1, self.beta2, self.eps)
-        on = (_pkg._ptr(grad_scale), _pkg._stream(stream, self.device))
+        call = self.state_bits, self.beta1, self.beta2, self.eps
+        on = _pkg._ptr(grad_scale), _pkg._stream(stream, self.device)
         late = self._late
         groups = (0,) if late is None else {k for k, g in zip(late, grads) if g is not None}
         for group in groups:  # of parameters at the same step of their own
@@ -231,6 +229,9 @@ class AdamW:
                 for e, k in zip(table, late):
                     e.n = e.n if k == group else 0
             rc = _pkg.lib().dflash2_adamw(table, len(table), *call, self.step_count + 1 - group, *on)
+            if rc == _UNSUPPORTED and _pkg._capturing(stream, self.device):
+                raise RuntimeError("an AdamW step cannot be captured: its replays would all be this step, with its "
+                                   "bias corrections and rates")
             _pkg._check("dflash2_adamw", rc)
         # written behind autograd's back: a backward through weights saved before must notice
         increment_version(self.params if whole else [p for p, g in zip(self.params, grads) if g is not None])

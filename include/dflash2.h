@@ -539,8 +539,8 @@ int dflash2_embedding_grad(const void* dout, int dout_dtype, int64_t dout_ld, co
  *   grad_scale  device fp32 scalar (a clip coefficient, 1 / tokens, a loss scale's
  *               inverse), nullable.  Where it is NaN or infinite the whole step is left
  *               out: nothing is written (whether it counts is up to the caller's next step).
- * step and the rates are read before the call returns: a call captured into a CUDA graph
- * repeats this very step at every replay, bias corrections included.
+ * step and the rates are the host's, so a graph's replays would all be one step: a stream
+ * that is being captured is DF2_ERR_UNSUPPORTED.
  * Rules: state_bits 32 or 8; 0 <= beta1, beta2 < 1; eps, lr, weight_decay finite and >= 0;
  * step >= 1 (1 = the first).  Tensors need only their elements' alignment (tensors whose
  * pointers are all 16-byte aligned run faster); no two buffers may overlap.

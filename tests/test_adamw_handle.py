@@ -18,13 +18,17 @@ class FakeLib:
     """Records the descriptors (copied) and the step of every dflash2_adamw call."""
 
     def __init__(self):
-        self.calls = []
+        self.calls, self.refuse = [], 0
+
+    def dflash2_status_string(self, code):
+        return b"refused"
 
     def dflash2_adamw(self, table, count, bits, beta1, beta2, eps, step, scale, stream):
         copy = (_abi.AdamWTensor * count)()
         ct.memmove(copy, table, ct.sizeof(copy))
-        self.calls.append((copy, step))
-        return 0
+        if not self.refuse:
+            self.calls.append((copy, step))
+        return self.refuse
 
 
 @pytest.fixture
@@ -193,13 +197,17 @@ def test_every_step_asks_for_the_current_device(fake, monkeypatch):
     assert len(fake.calls) == done + 1
 
 
-def test_a_step_is_not_captured(fake, monkeypatch):
+def test_a_refused_step_does_not_count(fake, monkeypatch):
+    """Under graph capture (where the library refuses) with the reason; otherwise by its status."""
     opt = handle(32)
     opt.step()
-    with monkeypatch.context() as m:
-        m.setattr(df2, "_capturing", lambda stream, device: True)
-        with pytest.raises(RuntimeError, match="captur"):
-            opt.step()
+    fake.refuse = 2
+    with pytest.raises(df2.DFlash2Error):
+        opt.step()
+    monkeypatch.setattr(df2, "_capturing", lambda stream, device: True)
+    with pytest.raises(RuntimeError, match="captur"):
+        opt.step()
+    fake.refuse = 0
     assert len(fake.calls) == 1 and opt.step_count == 1
     opt.step()
     assert fake.calls[-1][1] == 2
