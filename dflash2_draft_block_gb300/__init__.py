@@ -36,7 +36,7 @@ class DFlash2Error(RuntimeError):
 
 
 def lib():
-    return _abi.load()
+    return _abi._lib or _abi.load()
 
 
 def kernels_launched() -> int:
