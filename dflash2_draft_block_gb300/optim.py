@@ -91,6 +91,7 @@ class AdamW:
         self.beta1, self.beta2 = (float(b) for b in betas)
         self.lr, self.weight_decay = _each(lr, n, "lr"), _each(weight_decay, n, "weight_decay")
         self.device = self.params[0].device if n else None
+        self._cuda = self.device.index if n and self.device.type == "cuda" else None
         for i, p in enumerate(self.params):
             _tensor(p, f"params[{i}]", _DTYPES, None, self.device)
         if n:
@@ -215,7 +216,8 @@ class AdamW:
         whole = self._describe(grads)
         if not self.params:
             return
-        _pkg._device(self.params[0])
+        if self._cuda is None or torch.cuda.current_device() != self._cuda:
+            _pkg._device(self.params[0])  # refuses another device than the current one
         call = self.state_bits, self.beta1, self.beta2, self.eps
         on = _pkg._ptr(grad_scale), _pkg._stream(stream, self.device)
         late = self._late
