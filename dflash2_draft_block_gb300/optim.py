@@ -82,10 +82,10 @@ class AdamW:
         self.params = list(params)
         n = len(self.params)
         self.state_bits, self.eps = state_bits, float(eps)
-        steps = [int(t) for t in step] if isinstance(step, (list, tuple)) else [int(step)] * n
-        if len(steps) != n:
+        steps = [int(t) for t in step] if isinstance(step, (list, tuple)) else [int(step)] * max(n, 1)
+        if len(steps) != max(n, 1):
             raise ValueError(f"step must be one number or {n} of them, got {len(steps)}")
-        self.step_count = max(steps, default=0)
+        self.step_count = max(steps)
         # how many of them each parameter was left out of (None: none of any)
         self._late = [self.step_count - t for t in steps] if len(set(steps)) > 1 else None
         self.beta1, self.beta2 = (float(b) for b in betas)
@@ -102,10 +102,7 @@ class AdamW:
         self.state = self._fresh() if state is None else {k: list(state[k]) for k in _NAMES[state_bits]}
         self._check()
         self.grads = list(grads) if grads is not None else None
-        words = array("Q", bytes(8 * _WORDS * max(n, 1)))
-        self._table = (_abi.AdamWTensor * n).from_buffer(words)
-        self._words = {"Q": memoryview(words), "d": memoryview(words).cast("B").cast("d")}
-        self._seen = self._rates = None
+        self._table = self._words = self._seen = self._rates = None
 
     def _list(self, ts, name, dtype, per):
         if len(ts) != len(self.params):
@@ -154,10 +151,14 @@ class AdamW:
         params, n = self.params, len(self.params)
         if len(grads) != n:
             raise ValueError(f"{len(grads)} gradients for {n} parameters")
-        if n != len(self._table):
-            raise ValueError(f"the handle was made for {len(self._table)} parameters, now there are {n}")
         if n == 0:
             return True
+        if self._table is None:
+            words = array("Q", bytes(8 * _WORDS * n))
+            self._table = (_abi.AdamWTensor * n).from_buffer(words)
+            self._words = {"Q": memoryview(words), "d": memoryview(words).cast("B").cast("d")}
+        if n != len(self._table):
+            raise ValueError(f"the handle was made for {len(self._table)} parameters, now there are {n}")
         given, missing = grads, [i for i, g in enumerate(grads) if g is None]
         if missing:  # their parameters stand in, and their lengths become 0
             given = [p if g is None else g for p, g in zip(params, grads)]

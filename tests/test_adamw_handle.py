@@ -1,5 +1,6 @@
 """What the AdamW handle gives the library, on the CPU against a stand-in for it: the tensors
 and rates as they are at the step, every step checked, each parameter at its own step."""
+import copy
 import ctypes as ct
 import gc
 import weakref
@@ -24,10 +25,10 @@ class FakeLib:
         return b"refused"
 
     def dflash2_adamw(self, table, count, bits, beta1, beta2, eps, step, scale, stream):
-        copy = (_abi.AdamWTensor * count)()
-        ct.memmove(copy, table, ct.sizeof(copy))
+        held = (_abi.AdamWTensor * count)()
+        ct.memmove(held, table, ct.sizeof(held))
         if not self.refuse:
-            self.calls.append((copy, step))
+            self.calls.append((held, step))
         return self.refuse
 
 
@@ -261,9 +262,16 @@ def test_autograd_notices_a_step(fake):
     df2.AdamW([w], [zeros(4)]).step()                 # (keeps no version)
 
 
-def test_no_parameters(fake):
-    opt = df2.AdamW([], [])
+def test_a_handle_before_its_first_step_can_be_copied(fake):
+    opt = copy.deepcopy(handle(8))
     opt.step()
+    agree(opt, fake.calls[-1][0])
+
+
+def test_no_parameters(fake):
+    opt = df2.AdamW([], [], step=3)
+    opt.step()
+    assert opt.state_dict()["step"] == 3
     assert not fake.calls
     with pytest.raises(ValueError):
         opt.step([zeros(1)])
