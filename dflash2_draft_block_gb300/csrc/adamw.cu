@@ -23,10 +23,9 @@
 // and all of a lane's loads are issued before the first use, the gradient scale's among
 // them.  Four warps a CTA: its warps end together, and a smaller CTA gives way sooner (213
 // against 222 us with eight, 8-bit states of 78.8 M bf16 weights with masters: 6.7 TB/s;
-// the exact division instead of the fast one and the scale checked before the loads took
-// 280 us).  Two blocks a warp with the next one's loads in flight need 126 registers and
-// took 303 us.  States in fp32 with bf16 weights, gradients and masters: 42.9 M weights in
-// 175 us, 6.9 TB/s.
+// the exact division in the update, all else as it is, takes 238 us).  Two blocks a warp with
+// the next one's loads in flight need 126 registers and took 303 us.  States in fp32 with
+// bf16 weights, gradients and masters: 42.9 M weights in 175 us, 6.9 TB/s.
 // One launch covers up to kManyTensors tensors: their descriptors travel as the
 // kernel's parameters, so nothing is uploaded and no table of addresses outlives the
 // call; a warp finds its tensor by bisection over the block counts.

@@ -160,8 +160,10 @@ __device__ __forceinline__ void add4(float4* p, float4 x) {
 }
 
 // A row's columns = scale * f (+ themselves).  Added in fp32 by the memory's own add: a row
-// has one writer, so the result is the one rounded sum, and nobody waits for the old row
-// (the add flushes subnormal operands).
+// has one writer, so the result is the one rounded sum, and nobody waits for the old row.
+// The add takes subnormal operands, the row's own among them, for zero: at most 1.2e-38 is
+// lost a value.  Read, added and stored, which keeps them, 5,003 rows of 251 take 28.7 us
+// instead of 26.6, a selector's 512 rows of 16 at rank 256 40 to 43 instead of 38.
 template <bool OUT16, int W, int L>
 __device__ __forceinline__ void put_columns(char* p, int64_t left, float scale, bool accumulate, float4 x, float4 y) {
     float g[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
@@ -657,7 +659,8 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
             p.fill_rows[i] = int(dmax<int64_t>(1, rows));
             fill = (a.V + p.fill_rows[i] - 1) / p.fill_rows[i];
         }
-        if (fold > INT32_MAX || fill > INT32_MAX || p.chunks[i] * p.slices[i] > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+        if (fold > INT32_MAX || fill > INT32_MAX || p.chunks[i] * p.slices[i] > INT32_MAX / 2)
+            return cudaErrorInvalidConfiguration;
         p.fold_blocks[i] = int(fold);
         p.fills[i] = int(fill);
         blocks += fold;
@@ -669,7 +672,9 @@ cudaError_t fold_launch(const FoldArgs* jobs, int count, cudaStream_t stream) {
     if (blocks == 0) return cudaSuccess;
     if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     const bool s16 = jobs[0].src_bf16, o16 = jobs[0].out_bf16;
-#define DF2_FOLD(S, O)                                                                                          (vec ? (L == 8 ? launch<S, O, 8, 8>(p, small, blocks, stream) : launch<S, O, 8, 32>(p, small, blocks, stream))          : (L == 8 ? launch<S, O, 1, 8>(p, small, blocks, stream) : launch<S, O, 1, 32>(p, small, blocks, stream)))
+#define DF2_FOLD(S, O)                                                                                   \
+    (vec ? (L == 8 ? launch<S, O, 8, 8>(p, small, blocks, stream) : launch<S, O, 8, 32>(p, small, blocks, stream)) \
+         : (L == 8 ? launch<S, O, 1, 8>(p, small, blocks, stream) : launch<S, O, 1, 32>(p, small, blocks, stream)))
     if (s16) return o16 ? DF2_FOLD(true, true) : DF2_FOLD(true, false);
     return o16 ? DF2_FOLD(false, true) : DF2_FOLD(false, false);
 #undef DF2_FOLD
