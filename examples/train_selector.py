@@ -7,8 +7,7 @@ and the right token of a position is the candidate that follows best.  The unary
 do not know the table; the codebooks can learn it.  A step is
 
     h       = embedding(E, context)                     rows of the embedding by token id
-    ids, u  = unary_topk(h, W_lm, K)                    the candidates and their logits
-    G       = h W_H^T                                   (a plain matrix product)
+    ids, u, G = unary_topk(h, W_lm, K, W_H)             the candidates, their logits, h W_H^T
     loss, dscores, dG, dA, dBc = selector_loss_grad(...)
     dW_H    = dG^T h,  dh = dG W_H                      (plain matrix products)
     dE      = embedding_grad(dh, context)
@@ -49,11 +48,10 @@ def train(steps=60, positions=2048, vocab=4096, hidden=256, rank=64, top_k=16, s
         context[:: 16] = -1                                      # padding
         pred = torch.randint(0, classes, (positions,), generator=gen, device="cuda", dtype=torch.int32)
         h = df2.embedding(E, context, scale=scale)
-        ids, vals, _ = df2.unary_topk(h, W_lm, top_k)
+        ids, vals, G = df2.unary_topk(h, W_lm, top_k, W_H)
         column = follows[pred.long()].gather(1, ids.long() % classes).argmax(dim=1)
         targets = ids.gather(1, column[:, None])[:, 0]
         targets = torch.where(context < 0, torch.full_like(targets, -1), targets)
-        G = h.float() @ W_H.float().t()
         loss, label, dscores, dG, _, _ = df2.selector_loss_grad(pred, targets, ids, vals, G, A, Bc,
                                                                 dA=grads[2], dBc=grads[3])
         grads[1].copy_(dG.t() @ h.float())
