@@ -3,6 +3,8 @@
 Argument marshalling only: every step runs in the library's CUDA kernels.
 Tensors are torch CUDA tensors (bf16 weights/activations as torch.bfloat16),
 contiguous and row-major; calls are asynchronous on the current torch stream.
+Autograd records none of them: outputs do not require gradients, whatever the inputs
+do, and gradients come from the *_grad calls.
 
     ids, vals, G = unary_topk(h, W_lm, K, W_H)          # logits never leave the chip
     path, scores = selector_walk(anchors, ids, vals, G, A, Bc, block_size)

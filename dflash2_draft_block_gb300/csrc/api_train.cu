@@ -190,7 +190,11 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
         // does not know which rows the fold will write again: it clears a table of which
         // few rows can be written, the folds clear the others.  (16384 x 16 at rank 256: 123
         // us, 129 with both left to the folds, 125 with both cleared here; 4096 x 64 at rank
-        // 512: 156, 161, 166.)
+        // 512: 156, 161, 166.  Around the threshold, by this rule against both left to the
+        // folds, V = 1, 3, 4 and 8 N: 4096 x 16 at rank 256, fp32 tables: 55 92 121 204, 61 97
+        // 117 187; 2048 x 32, bf16: 49 60 75 116, 52 68 78 112; 1024 x 64 at rank 512, fp32: 83
+        // 158 220 386, 77 148 185 325.  So where the clearing is most of the work, past the
+        // threshold in fp32, the folds would be up to a fifth faster.)
         const bool beside_rows = P > 0 && 4 * N <= V;
         f.fill = !f.accumulate && !beside_rows;
         if (!f.accumulate && beside_rows) {

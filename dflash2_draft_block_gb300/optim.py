@@ -73,7 +73,8 @@ class AdamW:
     type and length.  Between steps the handle keeps no gradient that it was not made with.
 
     The states belong to the stream the handle was made on; `step` runs on `stream` (default:
-    the current one), and the caller orders the streams where they differ."""
+    the current one), and the caller orders the streams where they differ, and keeps the
+    gradients until such a step has read them."""
 
     def __init__(self, params, grads=None, *, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2,
                  state_bits=32, master_weights=None, state=None, step=0):
