@@ -136,11 +136,30 @@ def _check(call, rc):
         raise DFlash2Error(call, rc)
 
 
-def _workspace(nbytes, workspace, device):
+def _empty(shape, dtype, dev, stream):
+    """Memory for a call to write, of its stream's own: what the current stream's allocations
+    left free may have work queued there, which another stream does not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _made(shape, dtype, dev, stream):
+    """An output that the call makes: kept from other uses until the work of the current stream,
+    where the caller goes on with it, is done, too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    t = _empty(shape, dtype, dev, stream)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _workspace(nbytes, workspace, device, stream=None):
     if nbytes == 0 and workspace is None:
         return None
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return _empty(nbytes, torch.uint8, device, stream)
     _need(workspace, "workspace", workspace.dtype)
     if workspace.device != device:
         raise ValueError(f"workspace is on {workspace.device}, the call's tensors on {device}")
@@ -177,9 +196,9 @@ def unary_topk(h, W_lm, K, W_H=None, *, output_multiplier=1.0, final_logit_softc
             raise ValueError("W_H must be [r, D]")
     dev = _device(h, W_lm=W_lm, W_H=W_H)
     if out is None:
-        ids = torch.empty((P, K), dtype=torch.int32, device=dev)
-        vals = torch.empty((P, K), dtype=torch.float32, device=dev)
-        G = torch.empty((P, r), dtype=torch.float32, device=dev) if r else None
+        ids = _made((P, K), torch.int32, dev, stream)
+        vals = _made((P, K), torch.float32, dev, stream)
+        G = _made((P, r), torch.float32, dev, stream) if r else None
     else:
         ids, vals, G = out
         _out(ids, "ids", torch.int32, P * K, dev)
@@ -187,7 +206,7 @@ def unary_topk(h, W_lm, K, W_H=None, *, output_multiplier=1.0, final_logit_softc
         if r:
             _out(G, "G", torch.float32, P * r, dev)
     _status(dev_status, dev)
-    ws = _workspace(unary_topk_workspace_size(P, D, V, K, r), workspace, dev)
+    ws = _workspace(unary_topk_workspace_size(P, D, V, K, r), workspace, dev, stream)
     rc = lib().dflash2_unary_topk(_p(h), P, D, _p(W_lm), V, int(K), float(output_multiplier),
                                   float(final_logit_softcapping), _p(W_H), r, _p(G), _p(ids),
                                   _p(vals), _p(ws), _nbytes(ws),
@@ -215,9 +234,9 @@ def unary_topk_noalloc(h, W_lm, K, W_H=None, *, output_multiplier=1.0, final_log
             raise ValueError("W_H must be [r, D]")
     dev = _device(h, W_lm=W_lm, W_H=W_H)
     if out is None:
-        ids = torch.empty((P, K), dtype=torch.int32, device=dev)
-        vals = torch.empty((P, K), dtype=torch.float32, device=dev)
-        G = torch.empty((P, r), dtype=torch.float32, device=dev) if r else None
+        ids = _made((P, K), torch.int32, dev, stream)
+        vals = _made((P, K), torch.float32, dev, stream)
+        G = _made((P, r), torch.float32, dev, stream) if r else None
     else:
         ids, vals, G = out
         _out(ids, "ids", torch.int32, P * K, dev)
@@ -252,8 +271,8 @@ def selector_walk(anchors, topk_ids, topk_vals, G, A, Bc, block_size, *, dev_sta
     dev = _device(anchors, topk_ids=topk_ids, topk_vals=topk_vals, G=G, A=A, Bc=Bc)
     T = max(B - 1, 0)
     if out is None:
-        path = torch.empty((R, T), dtype=torch.int32, device=dev)
-        scores = torch.empty((R, T), dtype=torch.float32, device=dev)
+        path = _made((R, T), torch.int32, dev, stream)
+        scores = _made((R, T), torch.float32, dev, stream)
     else:
         path, scores = out
         _out(path, "path", torch.int32, R * T, dev)
@@ -279,8 +298,7 @@ def selector_ce(scores, topk_ids, targets, V, *, dev_status=None, out=None, stre
         raise ValueError("scores / topk_ids do not match [P, K]")
     dev = _device(scores, topk_ids=topk_ids, targets=targets)
     if out is None:
-        out = (torch.empty((P,), dtype=torch.float32, device=dev),
-               torch.empty((P,), dtype=torch.int32, device=dev))
+        out = (_made((P,), torch.float32, dev, stream), _made((P,), torch.int32, dev, stream))
     loss, label = out
     _out(loss, "loss", torch.float32, P, dev)
     _out(label, "label", torch.int32, P, dev)
@@ -309,7 +327,7 @@ def selector_pair_scores(pred, topk_ids, topk_vals, G, A, Bc, *, dev_status=None
         raise ValueError("Bc must be [V, r] like A")
     dev = _device(pred, topk_ids=topk_ids, topk_vals=topk_vals, G=G, A=A, Bc=Bc)
     if out is None:
-        scores = torch.empty((P, K), dtype=torch.float32, device=dev)
+        scores = _made((P, K), torch.float32, dev, stream)
     else:
         scores = _out(out, "scores", torch.float32, P * K, dev)
     _status(dev_status, dev)
@@ -351,11 +369,10 @@ def draft_head(h, W_lm, K, W_H, A, Bc, anchors, block_size, pred=None, *, output
     dev = _device(h, W_lm=W_lm, W_H=W_H, A=A, Bc=Bc, anchors=anchors, pred=pred)
     T = max(B - 1, 0)
     if out is None:
-        e = torch.empty
-        out = (e((P, K), dtype=torch.int32, device=dev), e((P, K), dtype=torch.float32, device=dev),
-               e((P, r), dtype=torch.float32, device=dev), e((R, T), dtype=torch.int32, device=dev),
-               e((R, T), dtype=torch.float32, device=dev),
-               e((P, K), dtype=torch.float32, device=dev) if pred is not None else None)
+        def e(shape, dtype):
+            return _made(shape, dtype, dev, stream)
+        out = (e((P, K), torch.int32), e((P, K), torch.float32), e((P, r), torch.float32), e((R, T), torch.int32),
+               e((R, T), torch.float32), e((P, K), torch.float32) if pred is not None else None)
     ids, vals, G, path, ps, pair = out
     _out(ids, "ids", torch.int32, P * K, dev)
     _out(vals, "vals", torch.float32, P * K, dev)
@@ -365,9 +382,9 @@ def draft_head(h, W_lm, K, W_H, A, Bc, anchors, block_size, pred=None, *, output
     if pred is not None:
         _out(pair, "pair_scores", torch.float32, P * K, dev)
     _status(dev_status, dev)
-    workspace = _workspace(draft_head_workspace_size(R, B, D, V, K, r), workspace, dev)
+    workspace = _workspace(draft_head_workspace_size(R, B, D, V, K, r), workspace, dev, stream)
     if workspace is None:  # nothing to hold (R = 0): the call still takes a buffer
-        workspace = torch.empty(1, dtype=torch.uint8, device=dev)
+        workspace = _empty(1, torch.uint8, dev, stream)
     rc = lib().dflash2_draft_head(_p(h), R, B, D, _p(W_lm), V, K, float(output_multiplier),
                                   float(final_logit_softcapping), _p(W_H), r, _p(A), _p(Bc), _p(anchors),
                                   _p(pred), _p(ids), _p(vals), _p(G), _p(path), _p(ps), _p(pair),
@@ -395,7 +412,7 @@ def selector_lattice(anchors, topk_ids, topk_vals, G, A, Bc, block_size, *, dev_
         raise ValueError("Bc must be [V, r] like A")
     dev = _device(anchors, topk_ids=topk_ids, topk_vals=topk_vals, G=G, A=A, Bc=Bc)
     T = max(B - 1, 0)
-    lat = out if out is not None else torch.empty((R, T, K, K), dtype=torch.float32, device=dev)
+    lat = out if out is not None else _made((R, T, K, K), torch.float32, dev, stream)
     _out(lat, "lattice", torch.float32, R * T * K * K, dev)
     _status(dev_status, dev)
     rc = lib().dflash2_selector_lattice(_p(anchors), R, B, _p(topk_ids), _p(topk_vals), _p(G), _p(A),
@@ -420,8 +437,8 @@ def lattice_walk(lattice, topk_ids, block_size, vocab_size, *, uniforms=None, te
             raise ValueError("uniforms must be [R, B-1]")
     dev = _device(lattice, topk_ids=topk_ids, uniforms=uniforms)
     if out is None:
-        path = torch.empty((R, T), dtype=torch.int32, device=dev)
-        scores = torch.empty((R, T), dtype=torch.float32, device=dev)
+        path = _made((R, T), torch.int32, dev, stream)
+        scores = _made((R, T), torch.float32, dev, stream)
     else:
         path, scores = out
         _out(path, "path", torch.int32, R * T, dev)
@@ -471,13 +488,13 @@ def conv_prepare(x, block_size, taps, group, W_proj, base, *, workspace=None, ou
     G = C // group if group >= 1 else 0
     dev = _device(x, W_proj=W_proj, base=base)
     if out is None:
-        y = torch.empty_like(x)
-        dyn = torch.empty((P, taps, G), dtype=torch.float32, device=dev)
+        y = _made(x.shape, x.dtype, dev, stream)
+        dyn = _made((P, taps, G), torch.float32, dev, stream)
     else:
         y, dyn = out
         _out(y, "y", x.dtype, P * C, dev)
         _out(dyn, "dyn_out", torch.float32, P * max(taps, 0) * G, dev)
-    ws = _workspace(conv_prepare_workspace_size(P, C, taps, group, dt), workspace, dev)
+    ws = _workspace(conv_prepare_workspace_size(P, C, taps, group, dt), workspace, dev, stream)
     rc = lib().dflash2_conv_prepare(_p(x), dt, P, C, int(block_size), taps, group,
                                     _p(W_proj), _p(base), _p(y), _p(dyn), _p(ws),
                                     _nbytes(ws), _stream(stream, dev))
@@ -495,7 +512,7 @@ def conv_finish(z, block_size, taps, group, dyn_out, base, *, out=None, stream=N
     taps, group = int(taps), int(group)
     _conv_shapes(C, taps, group, dyn_out=(dyn_out, P), base=(base, P))
     dev = _device(z, dyn_out=dyn_out, base=base)
-    y = _out(out, "y", z.dtype, P * C, dev) if out is not None else torch.empty_like(z)
+    y = _out(out, "y", z.dtype, P * C, dev) if out is not None else _made(z.shape, z.dtype, dev, stream)
     rc = lib().dflash2_conv_finish(_p(z), dt, P, C, int(block_size), taps, group,
                                    _p(dyn_out), _p(base), _p(y), _stream(stream, dev))
     _check("dflash2_conv_finish", rc)
@@ -524,14 +541,14 @@ def conv_finish_prepare(z, block_size, taps, group, dyn_out, base, W_proj, base_
     G = C // group if group >= 1 else 0
     dev = _device(z, dyn_out=dyn_out, base=base, W_proj=W_proj, base_next=base_next, residual=residual)
     if out is None:
-        h, y = torch.empty_like(z), torch.empty_like(z)
-        dyn = torch.empty((P, taps, G), dtype=torch.float32, device=dev)
+        h, y = _made(z.shape, z.dtype, dev, stream), _made(z.shape, z.dtype, dev, stream)
+        dyn = _made((P, taps, G), torch.float32, dev, stream)
     else:
         h, y, dyn = out
         _out(h, "h", z.dtype, P * C, dev)
         _out(y, "y_next", z.dtype, P * C, dev)
         _out(dyn, "dyn_out_next", torch.float32, P * max(taps, 0) * G, dev)
-    ws = _workspace(int(lib().dflash2_conv_finish_prepare_workspace_size(P, C, taps, group, dt)), workspace, dev)
+    ws = _workspace(int(lib().dflash2_conv_finish_prepare_workspace_size(P, C, taps, group, dt)), workspace, dev, stream)
     rc = lib().dflash2_conv_finish_prepare(_p(z), dt, P, C, int(block_size), taps, group, _p(dyn_out),
                                            _p(base), _p(residual), _p(h), _p(W_proj), _p(base_next), _p(y),
                                            _p(dyn), _p(ws), _nbytes(ws), _stream(stream, dev))
@@ -563,15 +580,6 @@ def _rows(t, name, shape=None, dev=None):
     return dt, ld
 
 
-def _empty(shape, dtype, dev, stream):
-    """Memory for a call to write, of its stream's own: what the current stream's allocations
-    left free may have work queued there, which another stream does not wait for."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
 def _scratch(nbytes, workspace, dev, stream):
     """The caller's workspace, or one of this call's own, free for the next call of the
     stream: (tensor, address, bytes)."""
@@ -582,16 +590,6 @@ def _scratch(nbytes, workspace, dev, stream):
         return None, 0, 0
     ws = _empty(nbytes, torch.uint8, dev, stream)
     return ws, ws.data_ptr(), nbytes
-
-
-def _made(shape, dtype, dev, stream):
-    """An output that the call makes: kept from other uses until the work of the current stream,
-    where the caller goes on with it, is done, too."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    t = _empty(shape, dtype, dev, stream)
-    t.record_stream(torch.cuda.current_stream(dev))
-    return t
 
 
 def _ptr(t):
