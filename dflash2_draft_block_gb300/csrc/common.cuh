@@ -6,6 +6,7 @@
 
 #include <climits>
 #include <cmath>
+#include <mutex>
 
 #include "dflash2.h"
 
@@ -16,6 +17,24 @@ namespace df2 {
 // Host side: count one kernel launch by this library (read back through
 // dflash2_kernels_launched).
 void note_launch();
+
+// Host side: allows a kernel `bytes` of dynamic shared memory on the current device.  The
+// allowance belongs to the kernel, not to a launch, so it is never lowered: another thread
+// may have asked for more and not launched yet.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    constexpr int kDevices = 64;
+    static std::mutex mu;
+    static size_t most[kDevices];  // allowed so far
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < kDevices && most[dev] > bytes) bytes = most[dev];
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (e == cudaSuccess && dev < kDevices) most[dev] = bytes;
+    return e;
+}
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 

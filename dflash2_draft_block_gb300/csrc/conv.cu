@@ -509,7 +509,7 @@ cudaError_t launch_t(const T* x, int64_t P, int C, int B, int taps, int g, const
 #define DF2_BULK(TP, R)                                                                                     \
     do {                                                                                                    \
         auto kern = conv_apply_bulk_kernel<T, TP, R>;                                                       \
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bp.smem));         \
+        e = allow_smem<conv_apply_bulk_kernel<T, TP, R>>(bp.smem);                                         \
         if (e != cudaSuccess) return e;                                                                    \
         e = cudaGetDevice(&dev);                                                                           \
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);        \
@@ -552,8 +552,7 @@ cudaError_t launch_t(const T* x, int64_t P, int C, int B, int taps, int g, const
         cudaError_t e = cudaSuccess;
 #define DF2_CONVA_R(TP, R)                                                                                  \
     do {                                                                                                    \
-        e = cudaFuncSetAttribute(conv_apply_async_kernel<T, TP, R>,                                         \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(async_smem));            \
+        e = allow_smem<conv_apply_async_kernel<T, TP, R>>(async_smem);                                      \
         if (e != cudaSuccess) return e;                                                                    \
         conv_apply_async_kernel<T, TP, R><<<agrid, nt, async_smem, stream>>>(                               \
             x, nblocks, C, B, g, G, strips, base, dyn, dyn_ld, res, y);                                    \
@@ -752,8 +751,7 @@ cudaError_t launch_prepare_rows(const T* x, int64_t P, int C, int B, int taps, i
     const int gpc = 2 * taps >= 8 ? 1 : 8 / (2 * taps);
     const size_t smem = size_t(PR) * C * sizeof(T) + size_t(PR) * taps * gpc * 4 +
                         size_t(kPrepWarps) * kPrepSums * 4;
-    cudaError_t e = cudaFuncSetAttribute(conv_prepare_rows_kernel<PG, T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_smem<conv_prepare_rows_kernel<PG, T>>(smem);
     if (e != cudaSuccess) return e;
     const dim3 grid = dim3(static_cast<unsigned>((G + gpc - 1) / gpc), static_cast<unsigned>((P + PR - 1) / PR));
     conv_prepare_rows_kernel<PG, T><<<grid, kPrepThreads, smem, stream>>>(x, P, C, B, taps, g, G, gpc, PR, W,

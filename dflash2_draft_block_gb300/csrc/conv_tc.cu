@@ -600,7 +600,7 @@ cudaError_t ctc_launch(const CUtensorMap& tx, const CUtensorMap& tw, const CUten
                        cudaStream_t stream) {
     const size_t smem = ctc_smem(a.nstages, TAPS, a.ng, PAIR, a.ds_ld) + 1024;
     auto kernel = conv_prepare_tc_kernel<TAPS, PAIR, MC>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_smem<conv_prepare_tc_kernel<TAPS, PAIR, MC>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((MC ? 4 : (PAIR ? 2 : 1)) * a.n_units));
@@ -622,8 +622,7 @@ cudaError_t ctc_launch(const CUtensorMap& tx, const CUtensorMap& tw, const CUten
 template <int TAPS>
 int ctc_mc_slots_t(size_t smem) {
     auto kernel = conv_prepare_tc_kernel<TAPS, true, true>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-        return 0;
+    if (allow_smem<conv_prepare_tc_kernel<TAPS, true, true>>(smem) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(4);
     cfg.blockDim = dim3(kCtcThreads);

@@ -255,7 +255,7 @@ cudaError_t launch_tail(int64_t P, int B, size_t smem, cudaStream_t stream, cons
                         float* path_scores, const int32_t* pred, float* pair_scores, int32_t* dev_status,
                         LogitMap lm, Refine rf, bool probe_only, bool* fits, int* max_clusters) {
     auto kernel = draft_tail_kernel<R, N, MINB>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_smem<draft_tail_kernel<R, N, MINB>>(smem);
     if (e != cudaSuccess) return e;
     if (B > 8) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);

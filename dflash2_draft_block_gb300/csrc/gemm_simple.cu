@@ -164,8 +164,7 @@ cudaError_t gemm_rows_launch(const void* X, bool x_f32, const uint16_t* W, int64
     const dim3 grid = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(groups));
     cudaError_t e = cudaSuccess;
 #define DF2_ROWS(PGV, T)                                                                            \
-    e = cudaFuncSetAttribute(gemm_rows_kernel<PGV, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
-                             int(smem));                                                            \
+    e = allow_smem<gemm_rows_kernel<PGV, T>>(smem);                                                 \
     if (e != cudaSuccess) return e;                                                                 \
     gemm_rows_kernel<PGV, T><<<grid, 256, smem, stream>>>(static_cast<const T*>(X), W, M, N, Kd,    \
                                                            out0, ld0, n_split, out1, ld1)

@@ -635,7 +635,7 @@ cudaError_t launch_wide(const CUtensorMap& ta, const CUtensorMap& tb, const CUte
     const int brows = PAIR ? BN / 2 : BN;
     const size_t smem = wide_smem(a.nstages, a.kbox, EPI, a.K, brows) + 1024;
     auto kernel = gemm_wide_kernel<EPI, BN, PAIR, GT, MC>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    cudaError_t e = allow_smem<gemm_wide_kernel<EPI, BN, PAIR, GT, MC>>(smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
@@ -688,7 +688,7 @@ int mc_cluster_slots(int K, int nstages) {
     const size_t smem = wide_smem(nstages, 1, EPI_TOPK, K, 128) + 1024;
     auto kernel = gemm_wide_kernel<EPI_TOPK, 256, true, false, true>;
     int n = 0;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) == cudaSuccess) {
+    if (allow_smem<gemm_wide_kernel<EPI_TOPK, 256, true, false, true>>(smem) == cudaSuccess) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(4);
         cfg.blockDim = dim3(kWideThreads);

@@ -210,8 +210,7 @@ cudaError_t head_simple_launch(const uint16_t* h, int64_t P, int64_t D, const ui
     switch (pl.PG) {
 #define DF2_CASE(PGV)                                                                          \
     case PGV:                                                                                  \
-        e = cudaFuncSetAttribute(head_simple_kernel<PGV>,                                      \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(pl.smem));    \
+        e = allow_smem<head_simple_kernel<PGV>>(pl.smem);                                      \
         if (e != cudaSuccess) return e;                                                        \
         head_simple_kernel<PGV><<<grid, kThreads, pl.smem, stream>>>(h, P, D, W, V, K,         \
                                                                     pl.chunk_rows, part_v,    \
@@ -232,8 +231,7 @@ cudaError_t head_simple_launch(const uint16_t* h, int64_t P, int64_t D, const ui
 cudaError_t topk_merge_launch(const float* part_v, const int* part_id, int S, int64_t P, int K,
                               int32_t* ids, float* vals, cudaStream_t stream, LogitMap lm) {
     const size_t msmem = size_t(kMergeChunk) * 8 + size_t(8) * K * 8 + 64;
-    cudaError_t e = cudaFuncSetAttribute(topk_merge_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(msmem));
+    cudaError_t e = allow_smem<topk_merge_kernel>(msmem);
     if (e != cudaSuccess) return e;
     topk_merge_kernel<<<unsigned(P), kThreads, msmem, stream>>>(part_v, part_id, S, P, K, ids, vals, lm);
     note_launch();

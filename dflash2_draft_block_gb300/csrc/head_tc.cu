@@ -470,8 +470,7 @@ int head_tc_launch(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W, i
     cudaError_t e = cudaSuccess;
 #define DF2_HEAD(NV, RV)                                                                          \
     do {                                                                                          \
-        e = cudaFuncSetAttribute(head_skinny_kernel<NV, RV>,                                      \
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));         \
+        e = allow_smem<head_skinny_kernel<NV, RV>>(smem);                                         \
         if (e != cudaSuccess) return DF2_ERR_CUDA;                                                \
         head_skinny_kernel<NV, RV><<<grid, kThreads, smem, stream>>>(                             \
             tm_w, tm_w2, tm_h, tm_wh, int(P), int(D), int(V), K, r, n_vtiles, vt.n_hi, vt.bm_hi,   \

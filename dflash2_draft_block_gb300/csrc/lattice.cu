@@ -484,8 +484,7 @@ cudaError_t lattice_launch(const int32_t* anchors, int R, int B, const int32_t* 
         // one slice buffer (the accumulator is staged over it at the end), then the
         // barriers, the TMEM address and the abort flag: eight CTAs fit on an SM
         const size_t smem = size_t(kLtcBuf) + 64 + 1024;
-        cudaError_t e = cudaFuncSetAttribute(lattice_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             int(smem));
+        cudaError_t e = allow_smem<lattice_tc_kernel>(smem);
         if (e != cudaSuccess) return e;
         lattice_tc_kernel<<<unsigned(int64_t(R) * T), kLtcThreads, smem, stream>>>(anchors, B, ids, vals, G, A, Bc,
                                                                                    V, K, r, lattice, dev_status);

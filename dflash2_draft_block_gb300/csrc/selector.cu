@@ -238,8 +238,7 @@ cudaError_t walk_launch(const int32_t* anchors, int R, int B, const int32_t* ids
     if (smem <= 200 * 1024) {
 #define DF2_WALK_CTA(N)                                                                             \
     do {                                                                                            \
-        cudaError_t e = cudaFuncSetAttribute(walk_cta_kernel<N>,                                    \
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)); \
+        cudaError_t e = allow_smem<walk_cta_kernel<N>>(smem);                                       \
         if (e != cudaSuccess) return e;                                                             \
         walk_cta_kernel<N><<<unsigned(R), kWalkThreads, smem, stream>>>(anchors, B, ids, vals, G, A,  \
                                                                         Bc, V, K, r, path, scores,   \

@@ -26,8 +26,7 @@ template <int R>
 cudaError_t launch_merge(const float* part_v, const int* part_id, int S, int64_t P, int K, int32_t* ids,
                          float* vals, cudaStream_t stream, LogitMap lm, Refine rf) {
     const size_t smem = merge_smem(S, K);
-    const cudaError_t e = cudaFuncSetAttribute(topk_merge_sorted_kernel<R>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const cudaError_t e = allow_smem<topk_merge_sorted_kernel<R>>(smem);
     if (e != cudaSuccess) return e;
     topk_merge_sorted_kernel<R><<<unsigned(P), kWarps * 32, smem, stream>>>(part_v, part_id, S, P, K, ids, vals,
                                                                            lm, rf);

@@ -1,4 +1,4 @@
-"""Host code of the training calls, compiled on the CPU from its own source text (taken out
+"""Host code of the launches, compiled on the CPU from its own source text (taken out
 of the .cu files by brace matching) against stand-ins for the CUDA runtime that record what
 they are asked.
 
@@ -6,6 +6,8 @@ they are asked.
   asks for it, and covers every call of that kernel.  (The allowance belongs to the kernel,
   not to the call: were it a call's own, one host thread could lower it between another's
   asking and launching.)
+- `allow_smem`, through which every other kernel asks: an allowance is never lowered, is each
+  device's and each kernel's own, and a refused one leaves the last.
 - `largest_cluster` of the sort: asked once a device, of each device for itself, and
   without memory from the C++ heap, whose exhaustion would leave the C entry as an
   exception.
@@ -91,7 +93,9 @@ const void* g_kernel;
 long long g_allowed, g_used;
 template <class K> cudaError_t cudaFuncSetAttribute(K* k, int which, int value) {
     g_kernel = reinterpret_cast<const void*>(k);
-    if (which == cudaFuncAttributeMaxDynamicSharedMemorySize) g_allowed = value;
+    if (which != cudaFuncAttributeMaxDynamicSharedMemorySize) return cudaSuccess;
+    if (value > 227 * 1024) return cudaErrorInvalidValue;
+    g_allowed = value;
     return cudaSuccess;
 }
 template <class K, class... A> cudaError_t cudaLaunchKernelEx(const cudaLaunchConfig_t* c, K* k, A&&...) {
@@ -167,6 +171,19 @@ extern "C" int cluster_of(int device, int fit, int no_memory, int* most, int* as
 """])
 
 
+def _allow_source():
+    return "template <auto Kernel>\n" + _block(_read("common.cuh"), "cudaError_t allow_smem(size_t bytes) {") + r"""
+void first_kernel(int) { g_used = 1; }
+void second_kernel(int) { g_used = 2; }
+extern "C" long long allowed(int second, int device, long long bytes) {
+    g_device = device;
+    g_allowed = -1;
+    const int rc = second ? allow_smem<second_kernel>(size_t(bytes)) : allow_smem<first_kernel>(size_t(bytes));
+    return rc == cudaSuccess ? g_allowed : -1;
+}
+"""
+
+
 @pytest.fixture(scope="module")
 def host(tmp_path_factory):
     cxx = shutil.which("g++")
@@ -174,7 +191,7 @@ def host(tmp_path_factory):
         pytest.skip("no g++")
     d = tmp_path_factory.mktemp("host_training")
     src, lib = d / "host.cpp", d / "host.so"
-    src.write_text(STUBS + _loss_source() + _sort_source())
+    src.write_text(STUBS + _loss_source() + _sort_source() + _allow_source())
     r = subprocess.run([cxx, "-std=c++17", "-O1", "-fPIC", "-shared", "-Wl,-Bsymbolic", "-o", str(lib), str(src)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     return ctypes.CDLL(str(lib))
@@ -198,6 +215,20 @@ def test_a_kernel_s_shared_memory_does_not_depend_on_the_call(host):
     for kernel, values in allowances.items():
         assert len(values) == 1, f"{len(values)} allowances, {min(values)} .. {max(values)}"
         assert largest[kernel] <= max(values) <= 227 * 1024
+
+
+def test_an_allowance_is_never_lowered(host):
+    host.allowed.restype = ctypes.c_longlong
+    ask = lambda second, device, bytes_: host.allowed(second, device, ctypes.c_longlong(bytes_))
+    assert ask(0, 0, 100_000) == 100_000 and ask(0, 0, 50_000) == 100_000
+    assert ask(0, 0, 227 * 1024 + 1) == -1 and ask(0, 0, 1) == 100_000
+    assert ask(0, 0, 150_000) == 150_000 and ask(0, 0, 100_000) == 150_000
+    assert ask(0, 3, 60_000) == 60_000 and ask(1, 0, 70_000) == 70_000
+    assert ask(0, 64, 80_000) == 80_000
+    # and nobody asks in another way, but for what does not depend on the call
+    for name in sorted(os.listdir(CSRC)):
+        if name not in ("common.cuh", "selector_loss.cu", "token_sort.cu"):
+            assert "cudaFuncAttributeMaxDynamicSharedMemorySize" not in _read(name), name
 
 
 def test_the_largest_cluster_of_each_device(host):
