@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes as ct
 import functools
+import operator
 
 import torch
 
@@ -24,6 +25,7 @@ from . import _abi
 
 DF2_DTYPE_BF16 = 0
 DF2_DTYPE_F32 = 1
+DF2_ERR_UNSUPPORTED = 2
 DF2_STATUS_ID_OUT_OF_RANGE = 0x1
 DF2_STATUS_WAIT_TIMEOUT = 0x2
 DF2_HEAD_PATH_STREAM = 0
@@ -731,6 +733,83 @@ def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weig
         dG.data_ptr(), _ptr(dA), _ptr(dBc), _DTYPES[dtype], ws, nbytes, _ptr(dev_status), _stream(stream, dev))
     _check("dflash2_selector_loss_grad", rc)
     return loss, label, ds, dG, dA, dBc
+
+
+def _random(rate, seed, draw, dev):
+    """rate, seed and draw as the library takes them: (rate, seed, draw, its address)."""
+    rate = float(rate)
+    if not 0.0 <= rate <= 1.0:
+        raise ValueError(f"rate must be in [0, 1], got {rate}")
+    seed = operator.index(seed)
+    if isinstance(draw, torch.Tensor):
+        _need(draw, "draw", torch.int64)
+        if draw.numel() != 1 or draw.device != dev:
+            raise ValueError("draw must be one int64 on the call's device")
+        number, at = 0, draw.data_ptr()
+    else:
+        number, at = operator.index(draw), 0
+    for name, v in (("seed", seed), ("draw", number)):
+        if not 0 <= v < 1 << 64:
+            raise ValueError(f"{name} must be in [0, 2^64), got {v}")
+    return rate, seed, number, at
+
+
+def dropout(x, rate, seed, draw=0, *, residual=None, dtype=None, out=None, stream=None):
+    """x with each element dropped with probability `rate` (in steps of 2^-16) and the others
+    scaled by 1 / (1 - rate), plus `residual`, in `dtype` (default: out's, or the residual's,
+    or x's).  The mask is a function of seed, draw and the element's index in x: nothing is stored,
+    dropout_grad makes it again, and another draw gives another mask.
+
+    draw: an integer, or an int64 tensor of one element on the GPU, read when the kernel
+    runs; a call that is being captured into a graph needs the tensor.  x, residual and out:
+    bf16 or fp32 matrices whose rows may be further apart than their length (residual of
+    out's type), or contiguous tensors of any shape.  out may be x or residual."""
+    shape = x.shape if isinstance(x, torch.Tensor) else None
+
+    def matrix(t, name):
+        # a contiguous tensor of any other shape is one row
+        if not isinstance(t, torch.Tensor) or t.shape != shape:
+            raise ValueError(f"{name} must have x's shape {list(shape)}, got {list(getattr(t, 'shape', []))}")
+        if t.dim() == 2:
+            return t
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be a matrix or contiguous")
+        return t.view(-1, t.shape[-1]) if t.dim() > 1 and t.numel() else t.view(1, -1)
+
+    if not isinstance(x, torch.Tensor) or not _on_device(x):
+        raise TypeError("x must be a CUDA tensor")
+    x2 = matrix(x, "x")
+    dt, ld = _rows(x2, "x")
+    dev = _device(x)
+    rate, seed, number, at = _random(rate, seed, draw, dev)
+    rdt, rld = (None, 0) if residual is None else _rows(matrix(residual, "residual"), "residual", dev=dev)
+    if out is None:
+        dtype = dtype if dtype is not None else (x if residual is None else residual).dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+        out = _made(shape, dtype, dev, stream)
+    odt, old = _rows(matrix(out, "out"), "out", dev=dev)
+    if dtype is not None and dtype != out.dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+    if rdt is not None and rdt != odt:
+        raise TypeError(f"residual must be {out.dtype} like the output, got {residual.dtype}")
+    if x.numel() == 0:
+        return out
+    rc = lib().dflash2_dropout(x.data_ptr(), dt, *x2.shape, ld, rate, seed, number, at, _ptr(residual), rld,
+                               out.data_ptr(), odt, old, _stream(stream, dev))
+    if rc == DF2_ERR_UNSUPPORTED and not at and _capturing(stream, dev):
+        raise RuntimeError("a captured dropout needs its draw as a tensor on the GPU: with a number every replay "
+                           "would drop the same elements")
+    _check("dflash2_dropout", rc)
+    return out
+
+
+def dropout_grad(dout, rate, seed, draw=0, *, dtype=None, accumulate=False, out=None, stream=None):
+    """The gradient of dropout()'s x: dropout() of dout with the same rate, seed and draw.
+    accumulate adds it to `out`.  (The residual's gradient is dout itself.)"""
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out: out must be given")
+    return dropout(dout, rate, seed, draw, residual=out if accumulate else None, dtype=dtype, out=out, stream=stream)
 
 
 from .optim import AdamW  # noqa: E402  (needs the checks above)

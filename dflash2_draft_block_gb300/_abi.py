@@ -11,7 +11,7 @@ import threading
 
 from .build import INCLUDE, LIB
 
-_f64 = ct.c_double
+_f64, _u64 = ct.c_double, ct.c_uint64
 _i64, _i32, _int, _vp, _sz, _f32 = ct.c_int64, ct.c_int32, ct.c_int, ct.c_void_p, ct.c_size_t, ct.c_float
 
 class AdamWTensor(ct.Structure):
@@ -60,6 +60,7 @@ SIGNATURES = {
     "dflash2_embedding_grad_workspace_size": (_sz, [_i64, _i64, _i64]),
     "dflash2_embedding_grad": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _f32, _int, _vp, _int, _i64, _vp, _sz,
                                       _vp, _vp]),
+    "dflash2_dropout": (_int, [_vp, _int, _i64, _i64, _i64, _f64, _u64, _u64, _vp, _vp, _i64, _vp, _int, _i64, _vp]),
     "dflash2_adamw": (_int, [_vp, _int, _int, _f64, _f64, _f64, _i64, _vp, _vp]),
 }
 

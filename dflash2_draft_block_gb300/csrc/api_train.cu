@@ -1,6 +1,7 @@
 // The C-ABI of the training calls: argument validation, workspace layout and dispatch.
 // Every rule checked here is stated beside the call in include/dflash2.h.
 #include <cfloat>
+#include <cmath>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -217,4 +218,47 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
         return DF2_ERR_CUDA;
     if (count && df2::fold_launch(jobs, count, st) != cudaSuccess) return DF2_ERR_CUDA;
     return DF2_OK;
+}
+
+// ---------------------------------------------------------------- dropout --
+
+namespace {
+
+// [N, D] elements `ld` apart a row: whether two such tensors share bytes.
+bool overlap(const void* p, int64_t p_ld, int p_dtype, const void* q, int64_t q_ld, int q_dtype, int64_t N, int64_t D) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const uintptr_t an = uintptr_t((N - 1) * p_ld + D) * (p_dtype == DF2_DTYPE_BF16 ? 2 : 4);
+    const uintptr_t bn = uintptr_t((N - 1) * q_ld + D) * (q_dtype == DF2_DTYPE_BF16 ? 2 : 4);
+    return a < b + bn && b < a + an;
+}
+
+}  // namespace
+
+DF2_API int dflash2_dropout(const void* x, int x_dtype, int64_t N, int64_t D, int64_t x_ld, double rate, uint64_t seed,
+                            uint64_t draw, const int64_t* draw_at, const void* residual, int64_t residual_ld, void* out,
+                            int out_dtype, int64_t out_ld, void* stream) {
+    if (!dtype_ok(x_dtype) || !dtype_ok(out_dtype) || !(rate >= 0.0 && rate <= 1.0)) return DF2_ERR_INVALID_ARGUMENT;
+    if (N < 0 || D < 1) return DF2_ERR_INVALID_ARGUMENT;
+    if (N > kMaxElements / D) return DF2_ERR_UNSUPPORTED;
+    if (x_ld < D || out_ld < D || (residual && residual_ld < D)) return DF2_ERR_INVALID_ARGUMENT;
+    if (N == 0) return DF2_OK;
+    if (!x || !out) return DF2_ERR_INVALID_ARGUMENT;
+    if (!element_aligned(x, x_dtype) || !element_aligned(out, out_dtype) || !element_aligned(residual, out_dtype) ||
+        (reinterpret_cast<uintptr_t>(draw_at) & 7u))
+        return DF2_ERR_UNSUPPORTED;
+    // in place is fine (an element is read before it is written), a shifted overlap is not
+    if (overlap(x, x_ld, x_dtype, out, out_ld, out_dtype, N, D) &&
+        !(x == out && x_dtype == out_dtype && (x_ld == out_ld || N == 1)))
+        return DF2_ERR_INVALID_ARGUMENT;
+    if (residual && overlap(residual, residual_ld, out_dtype, out, out_ld, out_dtype, N, D) &&
+        !(residual == out && (residual_ld == out_ld || N == 1)))
+        return DF2_ERR_INVALID_ARGUMENT;
+    const df2::DropoutArgs a{x, x_dtype == DF2_DTYPE_BF16, x_ld, N, D, uint32_t(std::floor(rate * 65536.0 + 0.5)), seed,
+                             draw, draw_at, residual, residual_ld, out, out_dtype == DF2_DTYPE_BF16, out_ld};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // a draw that is an argument would be the same in every replay of a graph
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (!draw_at && cudaStreamIsCapturing(st, &capture) != cudaSuccess) return DF2_ERR_CUDA;
+    if (capture != cudaStreamCaptureStatusNone) return DF2_ERR_UNSUPPORTED;
+    return df2::dropout_launch(a, st) == cudaSuccess ? DF2_OK : DF2_ERR_CUDA;
 }

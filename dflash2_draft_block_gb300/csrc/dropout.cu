@@ -1,0 +1,115 @@
+// dflash2_dropout: out = keep ? x * scale : 0 (+ residual), the mask made from a counter.
+//
+// Element i of the tensor (its index in [N, D], whatever the strides) is kept where the
+// 16-bit word i % 8 of Philox4x32-10(key = seed, counter = (i / 8, draw)) is at least
+// `drop` = round(rate * 65536): the mask is a function of the seed, the draw and i, so the
+// gradient makes it again and nothing is stored.  (Philox: Salmon, Moraes, Dror, Shaw,
+// "Parallel random numbers: as easy as 1, 2, 3", 2011; constants and rounds from there.)
+// One call gives 128 bits, so 16-bit words serve 8 elements; 32-bit words would double
+// the integer work of each element for a rate finer than 2^-16.
+//
+// Bound: HBM.  A thread owns the 8 elements of one counter: 16 bytes of bf16 a load.
+// Tensors off 16-byte boundaries (odd D or strides) go element by element: a warp makes
+// the masks of 32 counters, one a lane, as 8 bits each, and then walks the 256 elements
+// with its lanes side by side, each taking its bit from the lane that made it.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace df2 {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Args {
+    const void* x;
+    const void* res;
+    void* out;
+    int64_t x_ld, res_ld, out_ld;
+    int64_t total, D;         // elements; a row's (flat: all of them)
+    uint32_t drop;            // of 65536
+    float scale;
+    uint64_t seed, draw;
+    const int64_t* draw_at;
+};
+
+// The keep bits of counter q's 8 elements.
+__device__ __forceinline__ uint32_t keep8(uint64_t q, uint64_t draw, uint64_t seed, uint32_t drop) {
+    uint32_t c0 = uint32_t(q), c1 = uint32_t(q >> 32), c2 = uint32_t(draw), c3 = uint32_t(draw >> 32);
+    uint32_t k0 = uint32_t(seed), k1 = uint32_t(seed >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
+        c0 = uint32_t(b >> 32) ^ c1 ^ k0;
+        c1 = uint32_t(b);
+        c2 = uint32_t(a >> 32) ^ c3 ^ k1;
+        c3 = uint32_t(a);
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    const uint32_t c[4] = {c0, c1, c2, c3};
+    uint32_t m = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        m |= uint32_t((c[w] & 0xFFFFu) >= drop) << (2 * w);
+        m |= uint32_t((c[w] >> 16) >= drop) << (2 * w + 1);
+    }
+    return m;
+}
+
+template <bool B16>
+__device__ __forceinline__ float read1(const void* p, int64_t i) {
+    return B16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// One element at a time, any stride and alignment.
+template <bool IN16, bool OUT16, bool RES>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warp = int64_t(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t base = warp * 256;
+    if (base >= a.total) return;
+    const uint64_t draw = a.draw_at ? uint64_t(*a.draw_at) : a.draw;
+    const uint32_t mine = keep8(uint64_t(warp) * 32 + lane, draw, a.seed, a.drop);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t i = base + j * 32 + lane;
+        const uint32_t m = __shfl_sync(kFull, mine, j * 4 + (lane >> 3));
+        if (i >= a.total) continue;
+        const int64_t row = i / a.D, col = i - row * a.D;
+        float y = 0.f;
+        if ((m >> (lane & 7)) & 1u) y = __fmul_rn(read1<IN16>(a.x, row * a.x_ld + col), a.scale);
+        if (RES) y = __fadd_rn(y, read1<OUT16>(a.res, row * a.res_ld + col));
+        const int64_t o = row * a.out_ld + col;
+        if (OUT16) static_cast<uint16_t*>(a.out)[o] = f32_to_bf16_rn(y);
+        else static_cast<float*>(a.out)[o] = y;
+    }
+}
+
+template <bool IN16, bool OUT16, bool RES>
+cudaError_t launch(const Args& a, cudaStream_t stream) {
+    const int64_t warps = (a.total + 255) / 256, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
+    dropout_kernel<IN16, OUT16, RES><<<unsigned(grid), kThreads, 0, stream>>>(a);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t dropout_launch(const DropoutArgs& d, cudaStream_t stream) {
+    Args a{d.x, d.res, d.out, d.x_ld, d.res_ld, d.out_ld, d.N * d.D, d.D, d.drop,
+           d.drop < 65536 ? 65536.f / float(65536 - d.drop) : 0.f, d.seed, d.draw, d.draw_at};
+    const int kind = (d.x_bf16 ? 4 : 0) | (d.out_bf16 ? 2 : 0) | (d.res ? 1 : 0);
+    switch (kind) {
+        case 0: return launch<false, false, false>(a, stream);
+        case 1: return launch<false, false, true>(a, stream);
+        case 2: return launch<false, true, false>(a, stream);
+        case 3: return launch<false, true, true>(a, stream);
+        case 4: return launch<true, false, false>(a, stream);
+        case 5: return launch<true, false, true>(a, stream);
+        case 6: return launch<true, true, false>(a, stream);
+        default: return launch<true, true, true>(a, stream);
+    }
+}
+
+}  // namespace df2

@@ -145,6 +145,22 @@ struct EmbeddingArgs {
 };
 cudaError_t embedding_launch(const EmbeddingArgs& a, cudaStream_t stream);
 
+// ---- dropout by a counter, and the same mask on a gradient (dropout.cu)
+struct DropoutArgs {
+    const void* x;
+    bool x_bf16;
+    int64_t x_ld, N, D;
+    uint32_t drop;            // an element goes where its 16-bit word is below this
+    uint64_t seed, draw;
+    const int64_t* draw_at;   // nullable: the draw, on the device
+    const void* res;          // nullable, out's type
+    int64_t res_ld;
+    void* out;
+    bool out_bf16;
+    int64_t out_ld;
+};
+cudaError_t dropout_launch(const DropoutArgs& a, cudaStream_t stream);
+
 // ---- (id, position) pairs of N < 2^31 ids in order of id, then of position
 //      (token_sort.cu): id in the low word, V for an id that is no token (negative, or
 //      outside the table), which sort last

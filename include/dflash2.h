@@ -21,6 +21,7 @@
  *   dflash2_embedding             rows of a table by token id, scaled
  *   dflash2_embedding_grad        the table's gradient, by sorted tokens
  *   dflash2_adamw                 an AdamW step over many tensors
+ *   dflash2_dropout               dropout by a counter, and its gradient
  *
  * Sources (web pages, cited by title and section):
  *   [vLLM]  "DFlash2", vLLM Speculators user guide: "Local Convolution",
@@ -562,6 +563,39 @@ typedef struct {
 } dflash2_adamw_tensor;
 int dflash2_adamw(const dflash2_adamw_tensor* tensors, int count, int state_bits, double beta1, double beta2,
                   double eps, int64_t step, const float* grad_scale, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_dropout — dropout by a counter-based generator, with the residual's sum.
+ *
+ * No counterpart in the pages, which leave regularisation open.  For element i = n * D + d:
+ *   kept      where word[i] >= floor(rate * 65536 + 0.5) =: T
+ *   out[n, d] = (kept ? x[n, d] * (65536 / (65536 - T)) : 0) + residual[n, d]
+ * in fp32, rounded to out's dtype once.  word[i] is 16 bits of Philox4x32-10 (Salmon et al.,
+ * 2011) with the key seed (low word first) and the counter (i / 8 as two words, low first,
+ * then draw likewise): the low half of output word 0 for i % 8 = 0, its high half for 1, the
+ * low half of word 1 for 2, and so on.  So the mask depends on seed, draw and the element's
+ * index alone, not on types, strides or the launch, and is stored nowhere.  x is not used
+ * where it is dropped (a NaN there leaves no trace); T = 65536 drops everything.
+ *
+ * The gradient with respect to x is the same call on out's gradient (residual NULL, or the
+ * gradient to add to); that of residual is out's gradient itself.
+ *
+ *   x        [N, D] x_dtype, rows x_ld >= D elements apart
+ *   draw               which of the seed's masks: a step's and a layer's own number
+ *   draw_at            nullable: a device int64 that is read as the draw when the kernel runs
+ *                      (8-byte aligned), for graphs.  A stream that is being captured needs
+ *                      it: a draw that is an argument would give every replay one mask
+ *                      (DF2_ERR_UNSUPPORTED).
+ *   residual [N, D] out_dtype, rows residual_ld apart, nullable
+ *   out      [N, D] out_dtype, rows out_ld apart.  It may be x (same dtype and rows) or
+ *                      residual; any other overlap is DF2_ERR_INVALID_ARGUMENT.
+ * Rules: N >= 0, D >= 1, 0 <= rate <= 1; N * D <= 2^40 (else DF2_ERR_UNSUPPORTED).
+ * Tensors need only their elements' alignment; 16-byte aligned ones that are dense, or have
+ * D and strides a multiple of 8, run faster.
+ * ---------------------------------------------------------------------- */
+int dflash2_dropout(const void* x, int x_dtype, int64_t N, int64_t D, int64_t x_ld, double rate, uint64_t seed,
+                    uint64_t draw, const int64_t* draw_at, const void* residual, int64_t residual_ld, void* out,
+                    int out_dtype, int64_t out_ld, void* stream);
 
 /* ------------------------------------------------------------------------
  * dflash2_selftest_wait_timeout — exercises the in-kernel timeout path.
