@@ -748,9 +748,8 @@ def _random(rate, seed, draw, dev):
         number, at = 0, draw.data_ptr()
     else:
         number, at = operator.index(draw), 0
-    for name, v in (("seed", seed), ("draw", number)):
-        if not 0 <= v < 1 << 64:
-            raise ValueError(f"{name} must be in [0, 2^64), got {v}")
+    if not (0 <= seed < 1 << 64 and 0 <= number < 1 << 64):
+        raise ValueError(f"seed and draw must be in [0, 2^64), got {seed} and {number}")
     return rate, seed, number, at
 
 
@@ -764,39 +763,43 @@ def dropout(x, rate, seed, draw=0, *, residual=None, dtype=None, out=None, strea
     runs; a call that is being captured into a graph needs the tensor.  x, residual and out:
     bf16 or fp32 matrices whose rows may be further apart than their length (residual of
     out's type), or contiguous tensors of any shape.  out may be x or residual."""
-    shape = x.shape if isinstance(x, torch.Tensor) else None
-
-    def matrix(t, name):
-        # a contiguous tensor of any other shape is one row
-        if not isinstance(t, torch.Tensor) or t.shape != shape:
-            raise ValueError(f"{name} must have x's shape {list(shape)}, got {list(getattr(t, 'shape', []))}")
-        if t.dim() == 2:
-            return t
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be a matrix or contiguous")
-        return t.view(-1, t.shape[-1]) if t.dim() > 1 and t.numel() else t.view(1, -1)
-
     if not isinstance(x, torch.Tensor) or not _on_device(x):
         raise TypeError("x must be a CUDA tensor")
-    x2 = matrix(x, "x")
-    dt, ld = _rows(x2, "x")
     dev = _device(x)
     rate, seed, number, at = _random(rate, seed, draw, dev)
-    rdt, rld = (None, 0) if residual is None else _rows(matrix(residual, "residual"), "residual", dev=dev)
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or t.device != dev:
+                raise TypeError(f"{name} must be a tensor on {dev}")
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must have x's shape {list(x.shape)}, got {list(t.shape)}")
+    if out is not None:
+        if dtype is not None and dtype != out.dtype:
+            raise TypeError(f"out must be {dtype}, got {out.dtype}")
+        dtype = out.dtype
+    elif dtype is None:
+        dtype = (x if residual is None else residual).dtype
+    dt, odt = _DTYPES.get(x.dtype), _DTYPES.get(dtype)
+    if dt is None or odt is None:
+        raise TypeError(f"x and dtype must be bfloat16 or float32, got {x.dtype} and {dtype}")
+    if residual is not None and residual.dtype != dtype:
+        raise TypeError(f"residual must be {dtype} like the output, got {residual.dtype}")
+    dense = x.is_contiguous() and (residual is None or residual.is_contiguous()) and (out is None or out.is_contiguous())
+    if not dense and x.dim() != 2:
+        raise ValueError("x, residual and out must be matrices or contiguous")
     if out is None:
-        dtype = dtype if dtype is not None else (x if residual is None else residual).dtype
-        if dtype not in _DTYPES:
-            raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
-        out = _made(shape, dtype, dev, stream)
-    odt, old = _rows(matrix(out, "out"), "out", dev=dev)
-    if dtype is not None and dtype != out.dtype:
-        raise TypeError(f"out must be {dtype}, got {out.dtype}")
-    if rdt is not None and rdt != odt:
-        raise TypeError(f"residual must be {out.dtype} like the output, got {residual.dtype}")
-    if x.numel() == 0:
+        out = _made(x.shape, dtype, dev, stream)
+    if dense:  # one row
+        N, D = 1, x.numel()
+        ld = rld = old = D
+    else:
+        N, D = x.shape
+        ld, old = _rows(x, "x")[1], _rows(out, "out")[1]
+        rld = 0 if residual is None else _rows(residual, "residual")[1]
+    if N * D == 0:
         return out
-    rc = lib().dflash2_dropout(x.data_ptr(), dt, *x2.shape, ld, rate, seed, number, at, _ptr(residual), rld,
-                               out.data_ptr(), odt, old, _stream(stream, dev))
+    rc = lib().dflash2_dropout(x.data_ptr(), dt, N, D, ld, rate, seed, number, at, _ptr(residual), rld, out.data_ptr(),
+                               odt, old, _stream(stream, dev))
     if rc == DF2_ERR_UNSUPPORTED and not at and _capturing(stream, dev):
         raise RuntimeError("a captured dropout needs its draw as a tensor on the GPU: with a number every replay "
                            "would drop the same elements")

@@ -85,11 +85,110 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Args a) {
     }
 }
 
+// 8 consecutive elements as they lie in memory (16 bytes of bf16, 32 of fp32).
+template <bool B16>
+struct Eight {
+    uint4 a, b;
+    __device__ __forceinline__ void read(const void* p, int64_t i) {
+        const uint4* q = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + i * (B16 ? 2 : 4));
+        a = __ldcs(q);
+        if (!B16) b = __ldcs(q + 1);
+    }
+    __device__ __forceinline__ void to(float f[8]) const {
+        if (B16) {
+            unpack8(a, f);
+        } else {
+            f[0] = __uint_as_float(a.x); f[1] = __uint_as_float(a.y);
+            f[2] = __uint_as_float(a.z); f[3] = __uint_as_float(a.w);
+            f[4] = __uint_as_float(b.x); f[5] = __uint_as_float(b.y);
+            f[6] = __uint_as_float(b.z); f[7] = __uint_as_float(b.w);
+        }
+    }
+};
+
+// 8 elements a thread, `U` of them: FLAT tensors are one row (the last unit may be short),
+// others have rows of whole units.
+template <bool IN16, bool OUT16, bool RES, bool FLAT, int U>
+__global__ void __launch_bounds__(kThreads) dropout_units_kernel(const Args a, const int64_t units, const uint32_t per_row) {
+    const int64_t first = int64_t(blockIdx.x) * (kThreads * U) + threadIdx.x;
+    const uint64_t draw = a.draw_at ? uint64_t(*a.draw_at) : a.draw;
+    Eight<IN16> x[U];
+    Eight<OUT16> r[U];
+    int64_t row[U];
+    uint32_t unit[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int64_t q = first + k * kThreads;
+        row[k] = -1;
+        if (q >= units) continue;
+        if (FLAT) {
+            if (q * 8 + 8 > a.total) continue;  // the last, short unit
+            row[k] = 0;
+            x[k].read(a.x, q * 8);
+            if (RES) r[k].read(a.res, q * 8);
+        } else {
+            row[k] = units <= UINT32_MAX ? int64_t(uint32_t(q) / per_row) : q / per_row;
+            unit[k] = uint32_t(q - row[k] * per_row);
+            x[k].read(a.x, row[k] * a.x_ld + int64_t(unit[k]) * 8);
+            if (RES) r[k].read(a.res, row[k] * a.res_ld + int64_t(unit[k]) * 8);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int64_t q = first + k * kThreads;
+        if (q >= units) continue;
+        const uint32_t m = keep8(uint64_t(q), draw, a.seed, a.drop);
+        if (FLAT && row[k] < 0) {
+            for (int64_t i = q * 8; i < a.total; ++i) {
+                float y = (m >> (i & 7)) & 1u ? __fmul_rn(read1<IN16>(a.x, i), a.scale) : 0.f;
+                if (RES) y = __fadd_rn(y, read1<OUT16>(a.res, i));
+                if (OUT16) static_cast<uint16_t*>(a.out)[i] = f32_to_bf16_rn(y);
+                else static_cast<float*>(a.out)[i] = y;
+            }
+            continue;
+        }
+        float f[8], g[8];
+        x[k].to(f);
+        if (RES) r[k].to(g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = (m >> e) & 1u ? __fmul_rn(f[e], a.scale) : 0.f;
+            if (RES) f[e] = __fadd_rn(f[e], g[e]);
+        }
+        const int64_t o = FLAT ? q * 8 : row[k] * a.out_ld + int64_t(unit[k]) * 8;
+        if (OUT16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o) = make_uint4(
+                pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        } else {
+            float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+}
+
+bool lined_up(const void* p, int64_t ld, int64_t D, bool flat, bool b16) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (flat || (D % 8 == 0 && ld * (b16 ? 2 : 4) % 16 == 0));
+}
+
 template <bool IN16, bool OUT16, bool RES>
-cudaError_t launch(const Args& a, cudaStream_t stream) {
-    const int64_t warps = (a.total + 255) / 256, grid = (warps + kThreads / 32 - 1) / (kThreads / 32);
+cudaError_t launch(Args a, int64_t N, cudaStream_t stream) {
+    const bool flat = N == 1 || (a.x_ld == a.D && a.out_ld == a.D && (!RES || a.res_ld == a.D));
+    const bool units = lined_up(a.x, a.x_ld, a.D, flat, IN16) && lined_up(a.out, a.out_ld, a.D, flat, OUT16) &&
+                       (!RES || lined_up(a.res, a.res_ld, a.D, flat, OUT16)) && (flat || a.D / 8 <= UINT32_MAX);
+    if (flat) a.D = a.x_ld = a.out_ld = a.res_ld = a.total;
+    const int64_t n = units ? (a.total + 7) / 8 : (a.total + 255) / 256 * 32;  // threads' worth
+    // two units a thread once that still leaves every SM eight CTAs
+    const bool many = units && n >= int64_t(2) * kThreads * 8 * 152;
+    const int64_t per_cta = kThreads * (many ? 2 : 1), grid = (n + per_cta - 1) / per_cta;
     if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-    dropout_kernel<IN16, OUT16, RES><<<unsigned(grid), kThreads, 0, stream>>>(a);
+    const unsigned g = unsigned(grid);
+    const uint32_t row = uint32_t(flat ? 1 : a.D / 8);
+    if (!units) dropout_kernel<IN16, OUT16, RES><<<g, kThreads, 0, stream>>>(a);
+    else if (flat && many) dropout_units_kernel<IN16, OUT16, RES, true, 2><<<g, kThreads, 0, stream>>>(a, n, row);
+    else if (flat) dropout_units_kernel<IN16, OUT16, RES, true, 1><<<g, kThreads, 0, stream>>>(a, n, row);
+    else if (many) dropout_units_kernel<IN16, OUT16, RES, false, 2><<<g, kThreads, 0, stream>>>(a, n, row);
+    else dropout_units_kernel<IN16, OUT16, RES, false, 1><<<g, kThreads, 0, stream>>>(a, n, row);
     note_launch();
     return cudaGetLastError();
 }
@@ -101,14 +200,14 @@ cudaError_t dropout_launch(const DropoutArgs& d, cudaStream_t stream) {
            d.drop < 65536 ? 65536.f / float(65536 - d.drop) : 0.f, d.seed, d.draw, d.draw_at};
     const int kind = (d.x_bf16 ? 4 : 0) | (d.out_bf16 ? 2 : 0) | (d.res ? 1 : 0);
     switch (kind) {
-        case 0: return launch<false, false, false>(a, stream);
-        case 1: return launch<false, false, true>(a, stream);
-        case 2: return launch<false, true, false>(a, stream);
-        case 3: return launch<false, true, true>(a, stream);
-        case 4: return launch<true, false, false>(a, stream);
-        case 5: return launch<true, false, true>(a, stream);
-        case 6: return launch<true, true, false>(a, stream);
-        default: return launch<true, true, true>(a, stream);
+        case 0: return launch<false, false, false>(a, d.N, stream);
+        case 1: return launch<false, false, true>(a, d.N, stream);
+        case 2: return launch<false, true, false>(a, d.N, stream);
+        case 3: return launch<false, true, true>(a, d.N, stream);
+        case 4: return launch<true, false, false>(a, d.N, stream);
+        case 5: return launch<true, false, true>(a, d.N, stream);
+        case 6: return launch<true, true, false>(a, d.N, stream);
+        default: return launch<true, true, true>(a, d.N, stream);
     }
 }
 

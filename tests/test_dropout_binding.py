@@ -73,7 +73,7 @@ def test_valid_calls_reach_the_library(fake):
     name, a = fake.calls[-1]
     assert name == "dflash2_dropout" and a[1:8] == (0, 6, 24, 40, 0.1, 7, 3) and a[8] == 0
     assert df2.dropout(t(2, 3, 8), 0.5, (1 << 64) - 1).shape == (2, 3, 8)
-    assert fake.calls[-1][1][2:5] == (6, 8, 8)
+    assert fake.calls[-1][1][2:5] == (1, 48, 48)
     assert df2.dropout(t(5), 0.5, 0).shape == (5,)
     draw = torch.zeros(1, dtype=I64)
     df2.dropout(t(5, 8), 0.5, 0, draw)
