@@ -735,6 +735,93 @@ def selector_loss_grad(pred, targets, topk_ids, topk_vals, G, A, Bc, *, row_weig
     return loss, label, ds, dG, dA, dBc
 
 
+def _loss_inputs(h, W_lm, targets):
+    """The unary loss's inputs: (P, D, V, device)."""
+    _need(h, "h", torch.bfloat16, 2)
+    _need(W_lm, "W_lm", torch.bfloat16, 2)
+    _need(targets, "targets", torch.int32)
+    P, D = h.shape
+    if W_lm.shape[1] != D:
+        raise ValueError("W_lm must be [V, D]")
+    if targets.numel() != P:
+        raise ValueError(f"targets must be [P] ({P}), got {list(targets.shape)}")
+    return P, D, W_lm.shape[0], _device(h, W_lm=W_lm, targets=targets)
+
+
+def _loss_outputs(out, P, dev, stream):
+    if out is None:
+        return _made((P,), torch.float32, dev, stream), _made((P,), torch.float32, dev, stream)
+    loss, lse = out
+    _out(loss, "loss", torch.float32, P, dev)
+    if lse is not None:
+        _out(lse, "lse", torch.float32, P, dev)
+    return loss, lse
+
+
+def unary_ce_workspace_size(P, D, V) -> int:
+    return int(lib().dflash2_unary_ce_workspace_size(P, D, V))
+
+
+def unary_ce(h, W_lm, targets, *, output_multiplier=1.0, final_logit_softcapping=0.0, workspace=None, dev_status=None,
+             out=None, stream=None):
+    """The cross-entropy of unary_topk()'s logits over the whole vocabulary, which are never
+    stored: (loss [P], lse [P]), fp32, with lse the logarithm of each row's sum of exponentials.
+    Rows whose target is negative give NaN in both.  out: (loss, lse or None)."""
+    P, D, V, dev = _loss_inputs(h, W_lm, targets)
+    loss, lse = _loss_outputs(out, P, dev, stream)
+    _status(dev_status, dev)
+    _ws, ws, nbytes = _scratch(unary_ce_workspace_size(P, D, V), workspace, dev, stream)
+    rc = lib().dflash2_unary_ce(h.data_ptr(), P, D, W_lm.data_ptr(), V, float(output_multiplier),
+                                float(final_logit_softcapping), targets.data_ptr(), loss.data_ptr(), _ptr(lse), ws, nbytes,
+                                _ptr(dev_status), _stream(stream, dev))
+    _check("dflash2_unary_ce", rc)
+    return loss, lse
+
+
+def unary_loss_grad_workspace_size(P, D, V, dh=True, dW=False) -> int:
+    return int(lib().dflash2_unary_loss_grad_workspace_size(P, D, V, bool(dh), bool(dW)))
+
+
+def unary_loss_grad(h, W_lm, targets, *, row_weights=None, output_multiplier=1.0, final_logit_softcapping=0.0,
+                    accumulate=False, dh=True, dW=None, dtype=torch.bfloat16, workspace=None, dev_status=None, out=None,
+                    stream=None):
+    """unary_ce() and the gradients of sum(row_weights * loss): (loss [P], lse [P], dh [P, D],
+    dW [V, D]); rows without a target (negative) give NaN, a zero row of dh, and nothing to dW.
+
+    dh, dW: a tensor to write (dW: with accumulate to add to), True for a new one in
+    `dtype`, None to leave it out (dW by default: the head is the verifier's).  The factors of
+    the products are rounded to bf16 in either type.  out: (loss, lse or None)."""
+    P, D, V, dev = _loss_inputs(h, W_lm, targets)
+    if row_weights is not None:
+        _need(row_weights, "row_weights", torch.float32)
+        if row_weights.numel() != P or row_weights.device != dev:
+            raise ValueError("row_weights must be [P] on the call's device")
+    if accumulate and not isinstance(dW, torch.Tensor):
+        raise ValueError("accumulate adds to dW: it must be given")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
+    for name, t, n in (("dh", dh, P * D), ("dW", dW, V * D)):
+        if t is not None and t is not True:
+            if not isinstance(t, torch.Tensor) or t.dtype not in _DTYPES:
+                raise TypeError(f"{name} must be a bfloat16 or float32 CUDA tensor, True or None")
+            _out(t, name, t.dtype, n, dev)
+    if dh is True:
+        dh = _made((P, D), dtype, dev, stream)
+    if dW is True:
+        dW = _made((V, D), dtype, dev, stream)
+    loss, lse = _loss_outputs(out, P, dev, stream)
+    _status(dev_status, dev)
+    _ws, ws, nbytes = _scratch(unary_loss_grad_workspace_size(P, D, V, dh is not None, dW is not None), workspace, dev,
+                               stream)
+    rc = lib().dflash2_unary_loss_grad(
+        h.data_ptr(), P, D, W_lm.data_ptr(), V, float(output_multiplier), float(final_logit_softcapping),
+        targets.data_ptr(), _ptr(row_weights), bool(accumulate), loss.data_ptr(), _ptr(lse), _ptr(dh),
+        0 if dh is None else _DTYPES[dh.dtype], _ptr(dW), 0 if dW is None else _DTYPES[dW.dtype], ws, nbytes,
+        _ptr(dev_status), _stream(stream, dev))
+    _check("dflash2_unary_loss_grad", rc)
+    return loss, lse, dh, dW
+
+
 def _random(rate, seed, draw, dev):
     """rate, seed and draw as the library takes them: (rate, seed, draw, its address)."""
     rate = float(rate)

@@ -60,6 +60,11 @@ SIGNATURES = {
     "dflash2_embedding_grad_workspace_size": (_sz, [_i64, _i64, _i64]),
     "dflash2_embedding_grad": (_int, [_vp, _int, _i64, _vp, _i64, _i64, _i64, _f32, _int, _vp, _int, _i64, _vp, _sz,
                                       _vp, _vp]),
+    "dflash2_unary_ce_workspace_size": (_sz, [_i64, _i64, _i64]),
+    "dflash2_unary_ce": (_int, [_vp, _i64, _i64, _vp, _i64, _f32, _f32, _vp, _vp, _vp, _vp, _sz, _vp, _vp]),
+    "dflash2_unary_loss_grad_workspace_size": (_sz, [_i64, _i64, _i64, _int, _int]),
+    "dflash2_unary_loss_grad": (_int, [_vp, _i64, _i64, _vp, _i64, _f32, _f32, _vp, _vp, _int, _vp, _vp, _vp, _int,
+                                       _vp, _int, _vp, _sz, _vp, _vp]),
     "dflash2_dropout": (_int, [_vp, _int, _i64, _i64, _i64, _f64, _u64, _u64, _vp, _vp, _i64, _vp, _int, _i64, _vp]),
     "dflash2_adamw": (_int, [_vp, _int, _int, _f64, _f64, _f64, _i64, _vp, _vp]),
 }

@@ -145,6 +145,76 @@ struct EmbeddingArgs {
 };
 cudaError_t embedding_launch(const EmbeddingArgs& a, cudaStream_t stream);
 
+// ---- the cross entropy of the unary logits (unary_loss.cu, loss_gemm.cu).  Rows that have a
+//      target (live) are put next to each other first: count on the device says how many.  A
+//      piece is `rows` of them from row0 on.
+struct LossRowsArgs {
+    const int32_t* targets;
+    int64_t P, V, D;
+    const uint16_t* h;
+    uint16_t* live_h;         // [P rounded up to 64, D]: also zeros up to a multiple of 64 rows
+    int32_t* live_targets;    // [P]
+    int32_t* map;             // [P]: their rows in h
+    int32_t* count;
+    float* loss;              // [P]: NaN for the others
+    float* lse;               // the same, nullable
+    void* dh;                 // nullable: zeros for the others
+    bool dh_bf16;
+    int32_t* status;
+};
+cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream);
+
+struct LossGemmArgs {
+    const int32_t* count;
+    int64_t row0;
+    int rows;
+    int64_t V, D;
+    const int32_t* map;
+    int32_t* status;
+    // logits
+    const int32_t* targets;   // live_targets
+    float* target_logit;      // [P], of the live rows
+    float2* stats;            // [rows, n_stats]: (M, sum of exp(x - M)) of 128 columns each
+    int n_stats;
+    LogitMap lm;
+    uint16_t* e;              // [rows, e_ld], nullable
+    int64_t e_ld;
+    // the gradients: dh rows by map, or their parts [splits, part_rows, D]; dW
+    void* out;
+    bool out_bf16;
+    float* part;
+    int64_t part_rows;
+    float* sums;              // [V, D] between the pieces of one call, nullable where there is one
+    bool first, last, accumulate;
+};
+int loss_dh_splits(int64_t rows, int64_t D, int64_t V, int num_sms);
+cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t h_rows, const uint16_t* W, int num_sms,
+                               cudaStream_t stream);
+cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int splits, int num_sms,
+                           cudaStream_t stream);
+cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
+                           cudaStream_t stream);
+cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, int splits, cudaStream_t stream);
+
+struct LossRowArgs {
+    const int32_t* count;
+    int64_t row0;
+    int rows;
+    int64_t V;
+    const float2* stats;
+    int n_stats;
+    const float* target_logit;
+    const int32_t* live_targets;
+    const int32_t* map;
+    const float* weights;     // [P], nullable
+    LogitMap lm;
+    float* loss;
+    float* lse;
+    uint16_t* e;              // nullable; becomes the gradient of the logits, and zeros up to a
+    int64_t e_ld;             // multiple of 64 rows
+};
+cudaError_t loss_row_launch(const LossRowArgs& a, int64_t e_rows, int num_sms, cudaStream_t stream);
+
 // ---- dropout by a counter, and the same mask on a gradient (dropout.cu)
 struct DropoutArgs {
     const void* x;

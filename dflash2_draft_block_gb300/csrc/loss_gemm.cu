@@ -1,0 +1,491 @@
+// The matrix products of the unary loss on the tensor cores, CTA pairs on 256 x 256 tiles
+// (tcgen05.mma.cta_group::2, bf16 in, fp32 sums), with three epilogues:
+//   LOGITS  u = h W^T, never stored: of each row's 128 columns the largest logit M and the sum
+//           of exp(u - M) over the columns other than the target's, and the target's logit.
+//           With `e`, also exp(u - M) itself (times the softcap's slope) as bf16.
+//   DH      dh = g W:    A = g (K-major: its rows run along K = V), B = W, MN-major
+//   DW      dW = g^T h:  A = g, B = h, both MN-major (K = rows)
+// An MN-major operand is staged as panels of 64 M (or N) elements by 64 K rows, as TMA's
+// 128-byte swizzle writes a 64-element wide box: within a panel 8 K rows are 1024 bytes (the
+// descriptor's stride offset), panels follow each other (its leading offset), and 16 K
+// elements on are 2048 bytes.
+//
+// Sums in pieces.  The tensor core cuts each partial sum off below its last bit instead of
+// rounding it, so a sum of n steps drifts towards zero by about n / 4 ulp: a logit of 4096
+// products came out 4e-6 of itself too small, which a loss would show.  The MMAs
+// therefore sum kSegment K elements at a time into one of two TMEM accumulators while the
+// epilogue warps add the other to running sums in fp32 registers (128 columns a thread, eight
+// warps), rounded to nearest.
+//
+// Roles (320 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 2-9
+// are the epilogue (TMEM lane = row; two warps a quarter, 128 columns each).  Tiles are
+// dealt round-robin to the pairs.  Rows without a target were left out beforehand, so the
+// number of rows is read from the device.  All waits are bounded.
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tc_pair.cuh"
+#include "tc_ptx.cuh"
+
+namespace df2 {
+namespace {
+
+constexpr int kThreads = 320;
+constexpr int kTile = 256;
+constexpr int kStep = 64;                      // K elements a stage
+constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
+constexpr int kStages = 7;
+constexpr int kSegment = 8;                    // stages to a partial sum (512 K elements)
+constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
+constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
+
+enum { LOGITS, DH, DW };
+
+struct Work {
+    LossGemmArgs a;
+    int n_nt, splits;
+};
+
+// K-major as tc::sw128_kmajor_desc; MN-major: panels kStep * 128 bytes apart.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+    uint64_t d = tc::sw128_kmajor_desc(addr);
+    if (mn) d = (d & ~(uint64_t(0x3FFF) << 16)) | (uint64_t(kStep * 128 >> 4) << 16);
+    return d;
+}
+
+// 32 lanes x 32 consecutive columns, ready on return.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// One row's 128 logits of a tile (x, raw): the statistics, and e where asked.
+template <bool E>
+__device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[128], int row, int nt, int half) {
+    const int64_t c0 = int64_t(nt) * kTile + half * 128;
+    const int64_t t = a.targets[a.row0 + row] - c0;
+    const float cap = a.lm.cap;
+    if (!a.lm.identity()) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) x[j] = a.lm(x[j]);
+    }
+    if (t >= 0 && t < 128) {
+        float xt = 0.f;
+#pragma unroll
+        for (int j = 0; j < 128; ++j) {
+            int at = int(t);
+            asm volatile("" : "+r"(at));  // compared 128 times: an index would move x out of the registers
+            xt = j == at ? x[j] : xt;
+            x[j] = j == at ? -INFINITY : x[j];
+        }
+        a.target_logit[a.row0 + row] = xt;
+    }
+    if (c0 + 128 > a.V) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j)
+            if (c0 + j >= a.V) x[j] = -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 128; ++j) top = fmaxf(top, x[j]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
+    const float inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+#pragma unroll
+    for (int j0 = 0; j0 < 128; j0 += 8) {
+        float e[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = x[j0 + j];
+            e[j] = exp2f((v - base) * kLog2e);
+            sum[j & 3] += e[j];
+            if (E && cap > 0.f) {  // what is left out has e = 0 and no slope
+                const float bent = v == -INFINITY ? 0.f : v * inv_cap;
+                e[j] *= 1.f - bent * bent;
+            }
+        }
+        if (E)
+            *reinterpret_cast<uint4*>(out + j0) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
+                                                             pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+    }
+    a.stats[int64_t(row) * a.n_stats + nt * 2 + half] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+}
+
+// One row's columns [0, n) (n a multiple of 8) of sums to `out`, plus what is added to.
+__device__ __forceinline__ void write_row(float (&x)[128], int n, const float* add32, const void* add, void* out, bool b16) {
+#pragma unroll
+    for (int j0 = 0; j0 < 128; j0 += 8) {
+        if (j0 >= n) break;
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = x[j0 + j];
+        if (add32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] += add32[j0 + j];
+        }
+        if (b16) {
+            if (add) {
+                float o[8];
+                unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(add) + j0), o);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] += o[j];
+            }
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + j0) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        } else {
+            if (add) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] += static_cast<const float*>(add)[j0 + j];
+            }
+            float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + j0);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+        }
+    }
+}
+
+template <int MODE, bool E>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                 const __grid_constant__ Work w) {
+    constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
+    const LossGemmArgs& a = w.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + size_t(kStages) * 2 * kOperand);
+    uint64_t* empty = full + kStages;
+    uint64_t* tfull = empty + kStages;
+    uint64_t* tempty = tfull + 2;
+    uint64_t* mma_done = tempty + 2;
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = int(tc::cluster_ctarank());
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            tc::mbar_init(&full[s], 1);
+            tc::mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            tc::mbar_init(&tfull[b], 1);
+            tc::mbar_init(&tempty[b], 16);  // the epilogue warps of both CTAs
+        }
+        tc::mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        tc::fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc_pair(tmem_holder, 512);
+        tc::tmem_relinquish_pair();
+    }
+    if (warp == 0 && lane == 0) {
+        tc::prefetch_tmap(&tm_a);
+        tc::prefetch_tmap(&tm_b);
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::cluster_sync_all();
+    tc::fence_after_sync();
+    const uint32_t tmem_base = *tmem_holder;
+
+    // the rows of this piece that have a target
+    const int64_t left = int64_t(*a.count) - a.row0;
+    const int live = left < 0 ? 0 : left > a.rows ? a.rows : int(left);
+    const int n_mu = (int(MODE == DW ? a.V : live) + kTile - 1) / kTile;
+    const int total = n_mu * w.n_nt * w.splits;
+    const int k_total = (int(MODE == LOGITS ? a.D : MODE == DH ? a.V : live) + kStep - 1) / kStep;
+    const int units = int(gridDim.x) >> 1, unit = int(blockIdx.x) >> 1;
+
+    // tile i: its M unit, N tile and stages [k0, k1)
+    struct Tile {
+        int mu, nt, split, k0, k1;
+    };
+    auto tile = [&](int i) {
+        Tile t;
+        if (MODE == LOGITS) {  // M fastest: W streams past, h stays in L2
+            t.mu = i % n_mu;
+            t.nt = i / n_mu;
+            t.split = 0;
+        } else {               // N fastest: the pairs of a moment share g's rows
+            t.nt = i % w.n_nt;
+            const int rest = i / w.n_nt;
+            t.mu = rest % n_mu;
+            t.split = rest / n_mu;
+        }
+        t.k0 = int(int64_t(k_total) * t.split / w.splits);
+        t.k1 = int(int64_t(k_total) * (t.split + 1) / w.splits);
+        return t;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------------ TMA producer
+            const uint64_t keep = tc::l2_policy_evict_last(), pass = tc::l2_policy_evict_first();
+            const uint64_t pol_a = MODE == LOGITS ? keep : tc::l2_policy_evict_normal();
+            const uint64_t pol_b = MODE == LOGITS ? pass : MODE == DW ? keep : tc::l2_policy_evict_normal();
+            int stage = 0;
+            uint32_t phase = 0;
+            int8_t armed[kStages];
+            for (int s = 0; s < kStages; ++s) armed[s] = -1;
+            bool ok = true;
+            for (int i = unit; i < total && ok; i += units) {
+                const Tile t = tile(i);
+                for (int k = t.k0; k < t.k1; ++k) {
+                    if (!tc::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    if (leader) tc::mbar_arrive_expect_tx(&full[stage], 4 * kOperand);
+                    uint8_t* da = smem + size_t(stage) * 2 * kOperand;
+                    uint8_t* db = da + kOperand;
+                    const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), 0);
+                    const int ma = t.mu * kTile + rank * 128, nb = t.nt * kTile + rank * 128;
+                    if (MODE == LOGITS) {
+                        tc::tma_load_2d_pair(da, &tm_a, fb, k * kStep, int(a.row0) + ma, pol_a);
+                        tc::tma_load_2d_pair(db, &tm_b, fb, k * kStep, nb, pol_b);
+                    } else {
+                        if (A_MN) {
+                            tc::tma_load_2d_pair(da, &tm_a, fb, ma, k * kStep, pol_a);
+                            tc::tma_load_2d_pair(da + kOperand / 2, &tm_a, fb, ma + 64, k * kStep, pol_a);
+                        } else {
+                            tc::tma_load_2d_pair(da, &tm_a, fb, k * kStep, ma, pol_a);
+                        }
+                        const int kb = k * kStep + (MODE == DW ? int(a.row0) : 0);
+                        tc::tma_load_2d_pair(db, &tm_b, fb, nb, kb, pol_b);
+                        tc::tma_load_2d_pair(db + kOperand / 2, &tm_b, fb, nb + 64, kb, pol_b);
+                    }
+                    armed[stage] = int8_t(phase);
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok && leader) {
+                // wait (bounded) for the copies in flight; CTA 1's complete on CTA 0's barriers
+                // too, and it leaves only after the closing cluster barrier
+                volatile int never = 0;
+                for (int s = 0; s < kStages; ++s)
+                    if (armed[s] >= 0) tc::mbar_wait(&full[s], uint32_t(armed[s]), &never);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // -------------------------------------------------------- MMA issuer
+            constexpr uint32_t idesc =
+                tc::idesc_bf16_f32(256, 256) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, tphase = 0;
+            bool ok = true;
+            for (int i = unit; i < total && ok; i += units) {
+                const Tile t = tile(i);
+                for (int k = t.k0; k < t.k1 && ok; k += kSegment) {
+                    if (!tc::mbar_wait_cluster(&tempty[buf], tphase ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc::fence_after_sync();
+                    const uint32_t d = tmem_base + uint32_t(buf * kTile);
+                    const int end = min(k + kSegment, t.k1);
+                    for (int kk = k; kk < end; ++kk) {
+                        if (!tc::mbar_wait(&full[stage], phase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc::fence_after_sync();
+                        const uint32_t sa = tc::smem_u32(smem + size_t(stage) * 2 * kOperand), sb = sa + kOperand;
+#pragma unroll
+                        for (int q = 0; q < kStep / 16; ++q)
+                            tc::mma_bf16_pair(d, operand_desc(sa + q * (A_MN ? 2048 : 32), A_MN),
+                                              operand_desc(sb + q * (B_MN ? 2048 : 32), B_MN), idesc,
+                                              (kk != k || q != 0) ? 1u : 0u);
+                        tc::mma_commit_pair(&empty[stage], 0x3);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                    if (ok) tc::mma_commit_pair(&tfull[buf], 0x3);
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1;
+                }
+            }
+            tc::mma_commit_pair(mma_done, 0x3);
+            volatile int never = 0;
+            tc::mbar_wait(mma_done, 0, &never);
+        }
+    } else {
+        // ---------------------------------------------------------- epilogue
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        int buf = 0;
+        uint32_t tphase = 0;
+        bool ok = true;
+        for (int i = unit; i < total && ok; i += units) {
+            const Tile t = tile(i);
+            float x[128];
+#pragma unroll
+            for (int j = 0; j < 128; ++j) x[j] = 0.f;
+            for (int k = t.k0; k < t.k1; k += kSegment) {
+                ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
+                if (!ok) break;
+                tc::fence_after_sync();
+                const uint32_t taddr =
+                    tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + half * 128);
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    float v[32];
+                    tmem_ld32(taddr + c, v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) x[c + j] += v[j];
+                }
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), 0));
+                buf ^= 1;
+                if (buf == 0) tphase ^= 1;
+            }
+            if (!ok) break;
+            const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
+            if (MODE == LOGITS) {
+                if (m < live) logits_epilogue<E>(a, x, m, t.nt, half);
+            } else {
+                const int n0 = t.nt * kTile + half * 128;
+                const int n = min(128, int(a.D) - n0);
+                if (MODE == DH) {
+                    if (m < live && n > 0) {
+                        if (w.splits > 1) {
+                            float* part = a.part + (int64_t(t.split) * a.part_rows + m) * a.D + n0;
+                            write_row(x, n, nullptr, nullptr, part, false);
+                        } else {
+                            const int64_t o = int64_t(a.map[a.row0 + m]) * a.D + n0;
+                            write_row(x, n, nullptr, nullptr, static_cast<char*>(a.out) + o * (a.out_bf16 ? 2 : 4),
+                                      a.out_bf16);
+                        }
+                    }
+                } else if (m < a.V && n > 0) {
+                    const int64_t o = int64_t(m) * a.D + n0;
+                    const float* before = a.sums && !a.first ? a.sums + o : nullptr;
+                    if (!a.last) {
+                        write_row(x, n, before, nullptr, a.sums + o, false);
+                    } else {
+                        char* out = static_cast<char*>(a.out) + o * (a.out_bf16 ? 2 : 4);
+                        write_row(x, n, before, a.accumulate ? out : nullptr, out, a.out_bf16);
+                    }
+                }
+            }
+        }
+    }
+
+    tc::fence_before_sync();
+    __syncthreads();
+    // CTA 0's MMAs read this CTA's shared memory and write its TMEM: neither CTA frees TMEM or
+    // exits before both are done
+    tc::cluster_sync_all();
+    if (threadIdx.x == 0 && *abort_flag && a.status) atomicOr(a.status, DF2_STATUS_WAIT_TIMEOUT);
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// Boxes of 64 elements of a row by box_rows rows.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int MODE, bool E>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, int num_sms,
+                   cudaStream_t stream) {
+    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E>>(kSmem);
+    if (e != cudaSuccess) return e;
+    const int64_t pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
+    loss_gemm_kernel<MODE, E><<<unsigned(2 * pairs), kThreads, kSmem, stream>>>(ta, tb, w);
+    note_launch();
+    return cudaGetLastError();
+}
+
+int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
+
+}  // namespace
+
+int loss_dh_splits(int64_t rows, int64_t D, int64_t V, int num_sms) {
+    // the time of the busiest pair (a stage takes 0.3 us) and of writing and reading the
+    // partial sums at 4 TB/s
+    const int64_t tiles = up(rows, kTile) * up(D, kTile), steps = up(V, kStep), pairs = num_sms / 2;
+    int best = 1;
+    double least = 0.0;
+    for (int s = 1; s <= 64 && s <= up(steps, kSegment); ++s) {
+        double us = double(up(tiles * s, pairs)) * double(up(steps, s)) * 0.3;
+        if (s > 1) us += 3.0 + double(s) * double(rows) * double(D) * 8.0 / 4e6;
+        if (s == 1 || us < least) {
+            least = us;
+            best = s;
+        }
+    }
+    return best;
+}
+
+cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t h_rows, const uint16_t* W, int num_sms,
+                               cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!make_map(&ta, h, h_rows, a.D, a.D, 128) || !make_map(&tb, W, a.V, a.D, a.D, 128)) return cudaErrorInvalidValue;
+    const Work w{a, int(up(a.V, kTile)), 1};
+    const int64_t tiles = up(a.rows, kTile) * w.n_nt;
+    return a.e ? launch<LOGITS, true>(ta, tb, w, tiles, num_sms, stream)
+               : launch<LOGITS, false>(ta, tb, w, tiles, num_sms, stream);
+}
+
+cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int splits, int num_sms,
+                           cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
+    const Work w{a, int(up(a.D, kTile)), splits};
+    return launch<DH, false>(ta, tb, w, up(a.rows, kTile) * w.n_nt * splits, num_sms, stream);
+}
+
+cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
+                           cudaStream_t stream) {
+    CUtensorMap ta, tb;
+    if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
+    const Work w{a, int(up(a.D, kTile)), 1};
+    return launch<DW, false>(ta, tb, w, up(a.V, kTile) * w.n_nt, num_sms, stream);
+}
+
+}  // namespace df2

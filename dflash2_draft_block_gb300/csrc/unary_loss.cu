@@ -1,0 +1,207 @@
+// The row-wise steps of the unary loss around its matrix products (loss_gemm.cu).
+//
+// With x the mapped logits of a row, t its target and M its largest logit, the loss is kept
+// free of cancellation by summing the others apart from the target:
+//   s = sum over v != t of exp(x_v - M),   loss = (M - x_t) + log1p(s + (exp(x_t - M) - 1))
+//   dloss/dx_t = -s / (s + exp(x_t - M)),  dloss/dx_v = exp(x_v - M) / (s + exp(x_t - M))
+// so a row that is all but certain keeps its small loss and gradient to fp32's precision.
+//
+//   live_rows_kernel   the rows that have a target, in order, copied next to each other: the
+//                      products neither compute the others nor meet a NaN in them
+//   row_loss_kernel    a row's loss from its tiles' statistics, and its e to g in place
+//   sum_parts_kernel   dh from the K splits' partial sums, in order
+#include "common.cuh"
+#include "kernels.h"
+
+namespace df2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <class T, class Op>
+__device__ __forceinline__ T block_reduce(T v, T* shared, Op op) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = op(v, __shfl_xor_sync(kFull, v, o));
+    __syncthreads();  // shared may still be read from the last time
+    if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = shared[0];
+#pragma unroll
+    for (int k = 1; k < kThreads / 32; ++k) v = op(v, shared[k]);
+    return v;
+}
+
+// A block looks after `each` rows; it counts the live ones before them by itself, so the
+// rows are put in order in one launch.
+__global__ void __launch_bounds__(kThreads)
+live_rows_kernel(const LossRowsArgs a, const int each) {
+    __shared__ int shared[kThreads / 32];
+    __shared__ int place[kThreads];  // of the block's rows: its place among the live, -1: none
+    __shared__ int so_far;
+    const int64_t first = int64_t(blockIdx.x) * each, last = dmin<int64_t>(first + each, a.P);
+    auto alive = [&](int64_t p) { const int t = a.targets[p]; return t >= 0 && t < a.V; };
+    int before = 0;
+    for (int64_t p = threadIdx.x; p < first; p += kThreads) before += alive(p);
+    before = block_reduce(before, shared, [](int x, int y) { return x + y; });
+    if (threadIdx.x < 32) {
+        for (int64_t p0 = first; p0 < last; p0 += 32) {
+            const int64_t p = p0 + threadIdx.x;
+            const bool in = p < last, is = in && alive(p);
+            const unsigned live = __ballot_sync(kFull, is);
+            const int at = before + __popc(live & ((1u << threadIdx.x) - 1));
+            if (in) place[p - first] = is ? at : -1;
+            if (is) {
+                a.map[at] = int(p);
+                a.live_targets[at] = a.targets[p];
+            } else if (in) {
+                a.loss[p] = __int_as_float(0x7fc00000);
+                if (a.lse) a.lse[p] = __int_as_float(0x7fc00000);
+                if (a.status && a.targets[p] >= 0) atomicOr(a.status, DF2_STATUS_ID_OUT_OF_RANGE);
+            }
+            before += __popc(live);
+        }
+        if (threadIdx.x == 0) {
+            so_far = before;
+            if (last == a.P) *a.count = before;
+        }
+    }
+    __syncthreads();
+    const int units = int(a.D / 8);  // of 16 bytes of bf16
+    const int dh_units = a.dh ? units * (a.dh_bf16 ? 1 : 2) : 0;
+    for (int64_t p = first; p < last; ++p) {
+        const int at = place[p - first];
+        if (at >= 0) {
+            const uint4* from = reinterpret_cast<const uint4*>(a.h + p * a.D);
+            uint4* to = reinterpret_cast<uint4*>(a.live_h + int64_t(at) * a.D);
+            for (int u = threadIdx.x; u < units; u += kThreads) to[u] = __ldcs(from + u);
+        } else {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(a.dh) + p * dh_units * 16);
+            for (int u = threadIdx.x; u < dh_units; u += kThreads) to[u] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    if (last == a.P) {  // rows of the last K step of dW's product
+        const int64_t total = so_far, end = (total + 63) / 64 * 64;
+        uint4* to = reinterpret_cast<uint4*>(a.live_h + total * a.D);
+        for (int64_t u = threadIdx.x; u < (end - total) * units; u += kThreads) to[u] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// grid (rows of the piece, column shares).  G: e becomes the gradient of the logits.
+template <bool G>
+__global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a) {
+    __shared__ float shared[kThreads / 32];
+    const int64_t left = int64_t(*a.count) - a.row0;
+    const int64_t live = left < 0 ? 0 : left > a.rows ? a.rows : left;
+    const int64_t row = blockIdx.x;
+    const int64_t share = (a.V + 2047) / 2048, c0 = 2048 * (share * blockIdx.y / gridDim.y);
+    const int64_t c1 = dmin<int64_t>(2048 * (share * (blockIdx.y + 1) / gridDim.y), a.V);
+    if (row >= live) {
+        if (G && row < (live + 63) / 64 * 64) {  // rows of the last K step of dW's product
+            uint16_t* e = a.e + row * a.e_ld;
+            for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += kThreads * 8)
+                *reinterpret_cast<uint4*>(e + c) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const float2* stats = a.stats + row * a.n_stats;
+    const float xt = a.target_logit[a.row0 + row];
+    float top = xt;
+    for (int i = threadIdx.x; i < a.n_stats; i += kThreads) top = fmaxf(top, stats[i].x);
+    top = block_reduce(top, shared, [](float x, float y) { return fmaxf(x, y); });
+    float sum = 0.f;
+    for (int i = threadIdx.x; i < a.n_stats; i += kThreads) {
+        const float2 s = stats[i];
+        if (s.y != 0.f) sum += s.y * exp2f((s.x - top) * kLog2e);  // no column: 0 at -inf
+    }
+    sum = block_reduce(sum, shared, [](float x, float y) { return x + y; });
+    const int64_t p = a.map[a.row0 + row];
+    const float all = sum + expf(xt - top);
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        a.loss[p] = (top - xt) + log1pf(sum + expm1f(xt - top));
+        if (a.lse) a.lse[p] = top + logf(all);
+    }
+    if (!G) return;
+    const float w = (a.weights ? a.weights[p] : 1.f) * a.lm.mul / all;
+    const float bent = a.lm.cap > 0.f ? xt / a.lm.cap : 0.f;
+    const float gt = -sum * w * (1.f - bent * bent);
+    const int64_t t = a.live_targets[a.row0 + row];
+    uint16_t* e = a.e + row * a.e_ld;
+    for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += kThreads * 8) {
+        float f[8];
+        unpack8(*reinterpret_cast<const uint4*>(e + c), f);
+        const float2 s = stats[c / 128];
+        const float by = s.x == -INFINITY ? w : w * exp2f((s.x - top) * kLog2e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = c + j == t ? gt : f[j] * by;
+        *reinterpret_cast<uint4*>(e + c) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    }
+}
+
+// A thread sums 4 columns of a row.
+__global__ void __launch_bounds__(kThreads)
+sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* map, const float* part, int splits,
+                 int64_t part_rows, int64_t D, void* dh, bool bf16) {
+    const int64_t left = int64_t(*count) - row0;
+    const int64_t live = left < 0 ? 0 : left > rows ? rows : left;
+    const int64_t row = blockIdx.x;
+    if (row >= live) return;
+    const int64_t p = map[row0 + row];
+    for (int64_t d = 4 * (int64_t(blockIdx.y) * kThreads + threadIdx.x); d < D; d += 4 * int64_t(gridDim.y) * kThreads) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* from = part + row * D + d;
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * part_rows * D));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+        if (bf16) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dh) + p * D + d) =
+                make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+        } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(dh) + p * D + d) = s;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream) {
+    // few rows a block, so that a row's copy is not waited for by many; more of them where the
+    // blocks' own counting would be the longer part
+    int64_t each = (a.P + 4095) / 4096;
+    each = each < 4 ? 4 : each > kThreads ? kThreads : each;
+    const int64_t grid = (a.P + each - 1) / each;
+    live_rows_kernel<<<unsigned(grid), kThreads, 0, stream>>>(a, int(each));
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t loss_row_launch(const LossRowArgs& a, int64_t e_rows, int num_sms, cudaStream_t stream) {
+    if (!a.e) {
+        row_loss_kernel<false><<<unsigned(a.rows), kThreads, 0, stream>>>(a);
+    } else {
+        // columns shared out where the rows alone leave SMs idle
+        const int64_t rows = (a.rows + 63) / 64 * 64 < e_rows ? (a.rows + 63) / 64 * 64 : e_rows;
+        int64_t shares = (8 * num_sms + a.rows - 1) / a.rows;
+        const int64_t most = (a.V + 2047) / 2048;
+        shares = shares > most ? most : shares;
+        row_loss_kernel<true><<<dim3(unsigned(rows), unsigned(shares)), kThreads, 0, stream>>>(a);
+    }
+    note_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, int splits, cudaStream_t stream) {
+    const int64_t across = (a.D + 4 * kThreads - 1) / (4 * kThreads);
+    sum_parts_kernel<<<dim3(unsigned(a.rows), unsigned(across < 64 ? across : 64)), kThreads, 0, stream>>>(
+        a.count, a.row0, a.rows, a.map, a.part, splits, a.part_rows, a.D, a.out, a.out_bf16);
+    note_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace df2

@@ -18,6 +18,8 @@
  * and, for training the selector (each call says where it goes past the pages):
  *
  *   dflash2_selector_loss_grad    the selector's loss and its gradients
+ *   dflash2_unary_ce              the cross-entropy of the unary logits, full vocabulary
+ *   dflash2_unary_loss_grad       the same with the gradients of h and W_lm
  *   dflash2_embedding             rows of a table by token id, scaled
  *   dflash2_embedding_grad        the table's gradient, by sorted tokens
  *   dflash2_adamw                 an AdamW step over many tensors
@@ -468,6 +470,62 @@ int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int6
                                int32_t* label_idx, float* dscores, float* dG, void* dA, void* dBc,
                                int table_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_unary_ce — the cross-entropy of the unary logits over the whole vocabulary.
+ *
+ * The drafter's own loss: the logits of dflash2_unary_topk (the pages train the drafter on the
+ * verifier's tokens; they state the selector's loss only, this is the plain form).  With U'
+ * as dflash2_unary_topk defines it (multiplier and softcap) and t = targets[p]:
+ *   lse[p]  = log(sum_v exp(U'[p, v])),   loss[p] = lse[p] - U'[p, t]
+ * The logits are never stored.  Products are of the bf16 inputs; sums, maxima and the loss
+ * are fp32, and the loss of a row that is all but certain of its target does not cancel.
+ * A row without a target (targets[p] < 0) gives NaN in both and is not computed (its h may
+ * hold anything); a target >= V does the same and sets DF2_STATUS_ID_OUT_OF_RANGE.  A NaN or
+ * infinity in another row's h reaches that row's loss, and no other.
+ *
+ *   h [P, D] bf16; W_lm [V, D] bf16; targets [P] int32
+ *   loss [P] fp32 out; lse [P] fp32 out, nullable
+ *   workspace >= dflash2_unary_ce_workspace_size(P, D, V): a copy of h and at most 1 GiB of
+ *             statistics of 128 columns each (more rows go in pieces), or 256 rows' where those
+ *             are more
+ * Rules: P >= 0, V >= 1, D >= 1, D % 8 == 0; output_multiplier and final_logit_softcapping as
+ * dflash2_unary_topk; P < 2^31, V <= 2^24, D <= 2^20 (else DF2_ERR_UNSUPPORTED); outputs must
+ * not overlap inputs or one another.  h and W_lm 16-byte aligned, the rest by their elements.
+ * ---------------------------------------------------------------------- */
+size_t dflash2_unary_ce_workspace_size(int64_t P, int64_t D, int64_t V);
+int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_lm, int64_t V,
+                     float output_multiplier, float final_logit_softcapping, const int32_t* targets, float* loss,
+                     float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * dflash2_unary_loss_grad — dflash2_unary_ce with its gradients.
+ *
+ * With w = row_weights[p] (NULL: 1) and f(u) = c tanh(m u / c) (m u when c = 0) the logits' map:
+ *   g[p, v] = w * (exp(U'[p, v] - lse[p]) - [v == targets[p]]) * f'(U[p, v])
+ *   dh[p, :] = sum_v g[p, v] * W_lm[v, :];     dW[v, :] (+)= sum_p g[p, v] * h[p, :]
+ * loss is not weighted; the gradients are those of sum_p w_p * loss_p.  A row without a target
+ * contributes nothing: dh zero, its h and weight not used.
+ * The factors g are rounded to bf16 for the products, twice (as exp(U' - M), M the largest of
+ * 128 columns, and as g): 2^-8 of each, whatever the gradients' type.  Sums are fp32 in an
+ * order the shapes and the rows with a target fix, so equal inputs give equal bits; dh and dW
+ * are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it
+ * is written.
+ * Rows go in pieces of at most 4 GiB of such factors (or 256 rows' where those are more): the
+ * workspace does not grow with P beyond that but for a copy of h, and with dW the fp32 sums of
+ * V * D where there is more than one piece.
+ *
+ *   dh [P, D] dh_dtype, dW [V, D] dW_dtype, out, 16-byte aligned; NULL leaves one out (a frozen
+ *   head); the other arguments as dflash2_unary_ce.
+ *   workspace >= dflash2_unary_loss_grad_workspace_size(P, D, V, dh != NULL, dW != NULL)
+ * Rules as dflash2_unary_ce.
+ * ---------------------------------------------------------------------- */
+size_t dflash2_unary_loss_grad_workspace_size(int64_t P, int64_t D, int64_t V, int dh, int dW);
+int dflash2_unary_loss_grad(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_lm, int64_t V,
+                            float output_multiplier, float final_logit_softcapping, const int32_t* targets,
+                            const float* row_weights, int accumulate, float* loss, float* lse, void* dh, int dh_dtype,
+                            void* dW, int dW_dtype, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                            void* stream);
 
 /* ------------------------------------------------------------------------
  * dflash2_embedding — rows of a table by token id, scaled.
