@@ -164,6 +164,7 @@ struct LossRowsArgs {
 };
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream);
 
+constexpr float kExpScale = 32768.f;  // exp(x - M) is held in fp16 in units of 2^-15
 struct LossGemmArgs {
     const int32_t* count;
     int64_t row0;

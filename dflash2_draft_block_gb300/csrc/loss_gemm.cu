@@ -2,7 +2,7 @@
 // (tcgen05.mma.cta_group::2, bf16 in, fp32 sums), with three epilogues:
 //   LOGITS  u = h W^T, never stored: of each row's 128 columns the largest logit M and the sum
 //           of exp(u - M) over the columns other than the target's, and the target's logit.
-//           With `e`, also exp(u - M) itself (times the softcap's slope) as bf16.
+//           With `e`, also exp(u - M) itself (times the softcap's slope) as fp16.
 //   DH      dh = g W:    A = g (K-major: its rows run along K = V), B = W, MN-major
 //   DW      dW = g^T h:  A = g, B = h, both MN-major (K = rows)
 // An MN-major operand is staged as panels of 64 M (or N) elements by 64 K rows, as TMA's
@@ -17,7 +17,7 @@
 // epilogue warps add the other to running sums in fp32 registers (128 columns a thread, eight
 // warps), rounded to nearest.
 //
-// Roles (320 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 2-9
+// Roles (384 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-11
 // are the epilogue (TMEM lane = row; two warps a quarter, 128 columns each).  Tiles are
 // dealt round-robin to the pairs.  Rows without a target were left out beforehand, so the
 // number of rows is read from the device.  All waits are bounded.
@@ -31,12 +31,15 @@
 namespace df2 {
 namespace {
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers: launched with 168 a thread; the first four warps keep 88 and the epilogue's eight
+// take 208 (128 * 88 + 256 * 208 = 384 * 168).
+constexpr int kRoleRegisters = 88, kEpilogueRegisters = 208;
 constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
 constexpr int kStages = 7;
-constexpr int kSegment = 8;                    // stages to a partial sum (512 K elements)
+constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
 constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
 constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
 
@@ -74,89 +77,170 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// One row's 128 logits of a tile (x, raw): the statistics, and e where asked.
+// Two fp32 to a word of two fp16 (lo in the low half), to nearest even.
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+
+// The x held by a thread moves 32 places towards the front, the first 32 to the back.  Four
+// times is once around: a loop over 32 columns at a time that keeps x in registers.  (All 128
+// columns unrolled were thousands of instructions, read anew for every tile: 10 us of it.)
+__device__ __forceinline__ void turn(float (&x)[128]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const float first = x[j];
+        x[j] = x[j + 32];
+        x[j + 32] = x[j + 64];
+        x[j + 64] = x[j + 96];
+        x[j + 96] = first;
+    }
+}
+
+// cap * tanh(y), to about 2^-22 of it: tanh y = (E - 1) / (E + 1) with E = exp(2 y), and where
+// that would cancel the series y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835.
+__device__ __forceinline__ float bend(float y, float cap) {
+    const float e = exp2f(fminf(fmaxf(y, -20.f), 20.f) * (2.f * kLog2e));
+    const float wide = __fdividef(e - 1.f, e + 1.f);
+    const float q = y * y;
+    float s = fmaf(q, 0.021869488536155203f, -0.053968253968253970f);
+    s = fmaf(q, s, 0.13333333333333333f);
+    s = fmaf(q, s, -0.33333333333333333f);
+    const float near = fmaf(y * q, s, y);
+    const float b = fabsf(y) < 0.25f ? near : wide;
+    return __fmul_rn(cap, y == y ? b : y);
+}
+
+// 16 elements of bf16 or fp16, or 8 of fp32; `wide` (uniform): p is 32-byte aligned.
+__device__ __forceinline__ void store8(void* p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        uint4* q = static_cast<uint4*>(p);
+        q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+// One row's 128 logits of a tile (x, raw): the statistics, and e where asked, in fp16 in
+// units of 2^-15 (11 bits of exp(x - M) down to M - 20, then fewer until M - 27; bf16 here and
+// again as g would double the factors' rounding error).
 template <bool E>
 __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[128], int row, int nt, int half) {
     const int64_t c0 = int64_t(nt) * kTile + half * 128;
     const int64_t t = a.targets[a.row0 + row] - c0;
-    const float cap = a.lm.cap;
-    if (!a.lm.identity()) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j) x[j] = a.lm(x[j]);
-    }
-    if (t >= 0 && t < 128) {
+    const float cap = a.lm.cap, mul = cap > 0.f ? a.lm.mul / cap : a.lm.mul;
+    // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
+    auto map = [&](float u) { return cap > 0.f ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
+    if ((t >= 0 && t < 128) || c0 + 128 > a.V) {  // the target and what is no column are left out
+        const int end = c0 + 128 > a.V ? int(a.V - c0) : 128;
         float xt = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
 #pragma unroll
-        for (int j = 0; j < 128; ++j) {
-            int at = int(t);
-            asm volatile("" : "+r"(at));  // compared 128 times: an index would move x out of the registers
-            xt = j == at ? x[j] : xt;
-            x[j] = j == at ? -INFINITY : x[j];
+            for (int j = 0; j < 32; ++j) {
+                if (c + j == t) xt = x[j];
+                if (c + j == t || c + j >= end) x[j] = -INFINITY;
+            }
+            turn(x);
         }
-        a.target_logit[a.row0 + row] = xt;
-    }
-    if (c0 + 128 > a.V) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j)
-            if (c0 + j >= a.V) x[j] = -INFINITY;
+        if (t >= 0 && t < 128) a.target_logit[a.row0 + row] = map(xt);
     }
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 128; ++j) top = fmaxf(top, x[j]);
+    top = top == -INFINITY ? top : map(top);
     const float base = top == -INFINITY ? 0.f : top;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
     const float inv_cap = cap > 0.f ? 1.f / cap : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
 #pragma unroll
-    for (int j0 = 0; j0 < 128; j0 += 8) {
-        float e[8];
+        for (int j0 = 0; j0 < 32; j0 += 16) {
+            uint32_t word[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = x[j0 + j];
-            e[j] = exp2f((v - base) * kLog2e);
-            sum[j & 3] += e[j];
-            if (E && cap > 0.f) {  // what is left out has e = 0 and no slope
-                const float bent = v == -INFINITY ? 0.f : v * inv_cap;
-                e[j] *= 1.f - bent * bent;
+            for (int j = 0; j < 16; j += 2) {
+                float e[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float u = x[j0 + j + k], v = map(u);
+                    e[k] = u == -INFINITY ? 0.f : exp2f(__fmul_rn(__fsub_rn(v, base), kLog2e));
+                    sum[(j + k) & 3] = __fadd_rn(sum[(j + k) & 3], e[k]);
+                    if (E && cap > 0.f) {
+                        const float bent = v * inv_cap;
+                        e[k] *= 1.f - bent * bent;
+                    }
+                }
+                if (E) word[j / 2] = pack_f16(e[0] * kExpScale, e[1] * kExpScale);
             }
+            if (E) store8(out + c + j0, word, true);
         }
-        if (E)
-            *reinterpret_cast<uint4*>(out + j0) = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]),
-                                                             pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+        turn(x);
     }
     a.stats[int64_t(row) * a.n_stats + nt * 2 + half] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 // One row's columns [0, n) (n a multiple of 8) of sums to `out`, plus what is added to.
 __device__ __forceinline__ void write_row(float (&x)[128], int n, const float* add32, const void* add, void* out, bool b16) {
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll 1
+    for (int c = 0; c < n; c += 32) {
+        // the loads first, so that the loop waits once for all of them
+        uint4 f[8], g[8];
+        const int pieces = b16 ? 4 : 8;  // of 16 bytes
 #pragma unroll
-    for (int j0 = 0; j0 < 128; j0 += 8) {
-        if (j0 >= n) break;
-        float f[8];
+        for (int j = 0; j < 8; ++j) {
+            f[j] = add32 && c + 4 * j < n ? reinterpret_cast<const uint4*>(add32 + c)[j] : make_uint4(0u, 0u, 0u, 0u);
+            g[j] = add && j < pieces && c + (32 / pieces) * j < n
+                       ? reinterpret_cast<const uint4*>(static_cast<const char*>(add) + c * (b16 ? 2 : 4))[j]
+                       : make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = x[j0 + j];
-        if (add32) {
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] += add32[j0 + j];
+            for (int k = 0; k < 4; ++k) x[4 * j + k] += __uint_as_float(w[k]);
         }
         if (b16) {
-            if (add) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
                 float o[8];
-                unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(add) + j0), o);
+                unpack8(g[j], o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += o[j];
+                for (int k = 0; k < 8; ++k) x[8 * j + k] += o[k];
             }
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + j0) =
-                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
         } else {
-            if (add) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f[j] += static_cast<const float*>(add)[j0 + j];
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t w[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x[4 * j + k] += __uint_as_float(w[k]);
             }
-            float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + j0);
-            d[0] = make_float4(f[0], f[1], f[2], f[3]);
-            d[1] = make_float4(f[4], f[5], f[6], f[7]);
         }
+        if (b16) {
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 16) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[j0 + 2 * j], x[j0 + 2 * j + 1]);
+                uint16_t* to = static_cast<uint16_t*>(out) + c + j0;
+                if (c + j0 + 16 <= n) store8(to, w, wide);
+                else if (c + j0 < n) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        } else {
+#pragma unroll
+            for (int j0 = 0; j0 < 32; j0 += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[j0 + j]);
+                if (c + j0 < n) store8(static_cast<float*>(out) + c + j0, w, wide);
+            }
+        }
+        turn(x);
     }
 }
 
@@ -236,8 +320,9 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         return t;
     };
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegisters));
+        if (warp == 0 && lane == 0) {
             // ------------------------------------------------------ TMA producer
             const uint64_t keep = tc::l2_policy_evict_last(), pass = tc::l2_policy_evict_first();
             const uint64_t pol_a = MODE == LOGITS ? keep : tc::l2_policy_evict_normal();
@@ -288,8 +373,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     if (armed[s] >= 0) tc::mbar_wait(&full[s], uint32_t(armed[s]), &never);
             }
         }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (warp == 1 && lane == 0 && leader) {
             // -------------------------------------------------------- MMA issuer
             constexpr uint32_t idesc =
                 tc::idesc_bf16_f32(256, 256) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
@@ -335,7 +419,8 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         }
     } else {
         // ---------------------------------------------------------- epilogue
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegisters));
+        const int quarter = warp & 3, half = (warp >> 2) - 1;
         int buf = 0;
         uint32_t tphase = 0;
         bool ok = true;

@@ -10,6 +10,8 @@
 //                      products neither compute the others nor meet a NaN in them
 //   row_loss_kernel    a row's loss from its tiles' statistics, and its e to g in place
 //   sum_parts_kernel   dh from the K splits' partial sums, in order
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -18,6 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void unpack8_f16(const uint4& w, float f[8]) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(u + k));
+        f[2 * k] = v.x;
+        f[2 * k + 1] = v.y;
+    }
+}
 
 template <class T, class Op>
 __device__ __forceinline__ T block_reduce(T v, T* shared, Op op) {
@@ -123,15 +135,16 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
     }
     if (!G) return;
     const float w = (a.weights ? a.weights[p] : 1.f) * a.lm.mul / all;
+    const float w_e = w / kExpScale;
     const float bent = a.lm.cap > 0.f ? xt / a.lm.cap : 0.f;
     const float gt = -sum * w * (1.f - bent * bent);
     const int64_t t = a.live_targets[a.row0 + row];
     uint16_t* e = a.e + row * a.e_ld;
     for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += kThreads * 8) {
         float f[8];
-        unpack8(*reinterpret_cast<const uint4*>(e + c), f);
+        unpack8_f16(*reinterpret_cast<const uint4*>(e + c), f);
         const float2 s = stats[c / 128];
-        const float by = s.x == -INFINITY ? w : w * exp2f((s.x - top) * kLog2e);
+        const float by = s.x == -INFINITY ? w_e : w_e * exp2f((s.x - top) * kLog2e);
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[j] = c + j == t ? gt : f[j] * by;
         *reinterpret_cast<uint4*>(e + c) =
@@ -171,10 +184,9 @@ sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* ma
 }  // namespace
 
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream) {
-    // few rows a block, so that a row's copy is not waited for by many; more of them where the
-    // blocks' own counting would be the longer part
+    // a row a block, or more of them where the blocks' own counting would be the longer part
     int64_t each = (a.P + 4095) / 4096;
-    each = each < 4 ? 4 : each > kThreads ? kThreads : each;
+    if (each > kThreads) each = kThreads;
     const int64_t grid = (a.P + each - 1) / each;
     live_rows_kernel<<<unsigned(grid), kThreads, 0, stream>>>(a, int(each));
     note_launch();

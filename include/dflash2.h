@@ -506,8 +506,9 @@ int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_
  *   dh[p, :] = sum_v g[p, v] * W_lm[v, :];     dW[v, :] (+)= sum_p g[p, v] * h[p, :]
  * loss is not weighted; the gradients are those of sum_p w_p * loss_p.  A row without a target
  * contributes nothing: dh zero, its h and weight not used.
- * The factors g are rounded to bf16 for the products, twice (as exp(U' - M), M the largest of
- * 128 columns, and as g): 2^-8 of each, whatever the gradients' type.  Sums are fp32 in an
+ * The factors g are rounded to bf16 for the products (2^-8 of each), whatever the gradients'
+ * type, from exp(U' - M) held in fp16, M the largest of 128 columns (2^-11 of each, and 2^-40
+ * of the largest).  Sums are fp32 in an
  * order the shapes and the rows with a target fix, so equal inputs give equal bits; dh and dW
  * are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it
  * is written.

@@ -7,7 +7,8 @@ du = (D / 16 + 4) 2^-23 S.  The map multiplies by m (slope at most m) and rounds
 dx = m du + 2^-21 |x|.  exp turns dx, and the 2^-22 of its argument's product, into relative
 errors; a log-sum-exp is off by no more than its worst term, plus the rounding of sums of V
 terms in a tree of 128 columns a thread and of results of size |lse| and |x_t|.
-A factor g is exp(x - lse) to those relative errors, and rounded to bf16 twice (2^-8 each);
+A factor g is exp(x - lse) to those relative errors, rounded to fp16 (2^-11 of it, and in units of
+2^-39 of the largest of its 128 columns, which is at most the row's) and then to bf16 (2^-8);
 products of them are summed in n / 16 steps like the logits.
 """
 import torch
@@ -43,7 +44,7 @@ def reference(h, W, targets, weights=None, mul=1.0, cap=0.0, dW0=None):
     g.scatter_(1, t[:, None], -p_others[:, None])
     # the slope 1 - (x / c)^2 from a rounded x
     dslope = 2 * mul * x.abs() * dx / cap ** 2 + 2.0 ** -21 * mul if cap else torch.zeros_like(x)
-    dg = g.abs() * (slope * (rel + 2 * 2.0 ** -8 + 2.0 ** -15) + dslope)
+    dg = g.abs() * (slope * (rel + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15) + dslope) + mul * 2.0 ** -40 * torch.exp(top - lse)[:, None]
     g, dg = g * slope * w[:, None], dg * w.abs()[:, None] + 1e-38
     dh, dW = g @ W, g.T @ h
     ddh = (dg + (V / 16 + 4) * 2.0 ** -23 * g.abs()) @ W.abs()
