@@ -40,6 +40,10 @@ constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
 constexpr int kStages = 7;
 constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
+#ifndef KG
+#define KG 16
+#endif
+constexpr int kGroup = KG;                      // M units that share a pass over W
 constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
 constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
 
@@ -98,18 +102,24 @@ __device__ __forceinline__ void turn(float (&x)[128]) {
     }
 }
 
-// cap * tanh(y), to about 2^-22 of it: tanh y = (E - 1) / (E + 1) with E = exp(2 y), and where
-// that would cancel the series y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// cap * tanh(y), to about 2^-21 of it: tanh y = 1 - 2 / (exp(2 y) + 1), and where that would
+// cancel the series y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835.
 __device__ __forceinline__ float bend(float y, float cap) {
-    const float e = exp2f(fminf(fmaxf(y, -20.f), 20.f) * (2.f * kLog2e));
-    const float wide = __fdividef(e - 1.f, e + 1.f);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(y * (2.f * kLog2e)) + 1.f));
+    const float wide = fmaf(-2.f, r, 1.f);
     const float q = y * y;
     float s = fmaf(q, 0.021869488536155203f, -0.053968253968253970f);
     s = fmaf(q, s, 0.13333333333333333f);
     s = fmaf(q, s, -0.33333333333333333f);
     const float near = fmaf(y * q, s, y);
-    const float b = fabsf(y) < 0.25f ? near : wide;
-    return __fmul_rn(cap, y == y ? b : y);
+    return __fmul_rn(cap, fabsf(y) < 0.25f ? near : wide);
 }
 
 // 16 elements of bf16 or fp16, or 8 of fp32; `wide` (uniform): p is 32-byte aligned.
@@ -128,13 +138,13 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&w)[8], bool wid
 // One row's 128 logits of a tile (x, raw): the statistics, and e where asked, in fp16 in
 // units of 2^-15 (11 bits of exp(x - M) down to M - 20, then fewer until M - 27; bf16 here and
 // again as g would double the factors' rounding error).
-template <bool E>
+template <bool E, bool CAP>
 __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[128], int row, int nt, int half) {
     const int64_t c0 = int64_t(nt) * kTile + half * 128;
     const int64_t t = a.targets[a.row0 + row] - c0;
-    const float cap = a.lm.cap, mul = cap > 0.f ? a.lm.mul / cap : a.lm.mul;
+    const float cap = a.lm.cap, mul = CAP ? a.lm.mul / cap : a.lm.mul;
     // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
-    auto map = [&](float u) { return cap > 0.f ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
+    auto map = [&](float u) { return CAP ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
     if ((t >= 0 && t < 128) || c0 + 128 > a.V) {  // the target and what is no column are left out
         const int end = c0 + 128 > a.V ? int(a.V - c0) : 128;
         float xt = 0.f;
@@ -152,11 +162,13 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 128; ++j) top = fmaxf(top, x[j]);
-    top = top == -INFINITY ? top : map(top);
-    const float base = top == -INFINITY ? 0.f : top;
+    const bool none = top == -INFINITY;
+    // x - M in the units of the logits as they are mapped: without a cap the multiplier waits
+    const float base = none ? 0.f : CAP ? map(top) : top;
+    const float by = CAP ? kLog2e : __fmul_rn(kLog2e, mul);
+    const float inv_cap = CAP ? 1.f / cap : 0.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
-    const float inv_cap = cap > 0.f ? 1.f / cap : 0.f;
 #pragma unroll 1
     for (int c = 0; c < 128; c += 32) {
 #pragma unroll
@@ -167,21 +179,21 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
                 float e[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float u = x[j0 + j + k], v = map(u);
-                    e[k] = u == -INFINITY ? 0.f : exp2f(__fmul_rn(__fsub_rn(v, base), kLog2e));
+                    const float u = x[j0 + j + k], v = CAP ? map(u) : u;
+                    e[k] = exp2_fast(__fmul_rn(__fsub_rn(v, base), by));
+                    if (CAP && u == -INFINITY) e[k] = 0.f;
                     sum[(j + k) & 3] = __fadd_rn(sum[(j + k) & 3], e[k]);
-                    if (E && cap > 0.f) {
-                        const float bent = v * inv_cap;
-                        e[k] *= 1.f - bent * bent;
-                    }
+                    const float bent = v * inv_cap;
+                    e[k] *= CAP ? fmaf(-kExpScale * bent, bent, kExpScale) : kExpScale;
                 }
-                if (E) word[j / 2] = pack_f16(e[0] * kExpScale, e[1] * kExpScale);
+                if (E) word[j / 2] = pack_f16(e[0], e[1]);
             }
             if (E) store8(out + c + j0, word, true);
         }
         turn(x);
     }
-    a.stats[int64_t(row) * a.n_stats + nt * 2 + half] = make_float2(top, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    a.stats[int64_t(row) * a.n_stats + nt * 2 + half] =
+        make_float2(none ? top : CAP ? base : __fmul_rn(top, mul), (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 // One row's columns [0, n) (n a multiple of 8) of sums to `out`, plus what is added to.
@@ -244,7 +256,7 @@ __device__ __forceinline__ void write_row(float (&x)[128], int n, const float* a
     }
 }
 
-template <int MODE, bool E>
+template <int MODE, bool E, bool CAP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const __grid_constant__ Work w) {
@@ -305,9 +317,11 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     };
     auto tile = [&](int i) {
         Tile t;
-        if (MODE == LOGITS) {  // M fastest: W streams past, h stays in L2
-            t.mu = i % n_mu;
-            t.nt = i / n_mu;
+        if (MODE == LOGITS) {  // M fastest in groups: W streams past, a group's rows of h stay in L2
+            const int group = i / (kGroup * w.n_nt), first = group * kGroup;
+            const int wide = min(kGroup, n_mu - first), rest = i - first * w.n_nt;
+            t.mu = first + rest % wide;
+            t.nt = rest / wide;
             t.split = 0;
         } else {               // N fastest: the pairs of a moment share g's rows
             t.nt = i % w.n_nt;
@@ -451,7 +465,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             if (!ok) break;
             const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
             if (MODE == LOGITS) {
-                if (m < live) logits_epilogue<E>(a, x, m, t.nt, half);
+                if (m < live) logits_epilogue<E, CAP>(a, x, m, t.nt, half);
             } else {
                 const int n0 = t.nt * kTile + half * 128;
                 const int n = min(128, int(a.D) - n0);
@@ -515,13 +529,13 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool E>
+template <int MODE, bool E = false, bool CAP = false>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, int num_sms,
                    cudaStream_t stream) {
-    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E>>(kSmem);
+    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E, CAP>>(kSmem);
     if (e != cudaSuccess) return e;
     const int64_t pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
-    loss_gemm_kernel<MODE, E><<<unsigned(2 * pairs), kThreads, kSmem, stream>>>(ta, tb, w);
+    loss_gemm_kernel<MODE, E, CAP><<<unsigned(2 * pairs), kThreads, kSmem, stream>>>(ta, tb, w);
     note_launch();
     return cudaGetLastError();
 }
@@ -553,8 +567,11 @@ cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t
     if (!make_map(&ta, h, h_rows, a.D, a.D, 128) || !make_map(&tb, W, a.V, a.D, a.D, 128)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.V, kTile)), 1};
     const int64_t tiles = up(a.rows, kTile) * w.n_nt;
-    return a.e ? launch<LOGITS, true>(ta, tb, w, tiles, num_sms, stream)
-               : launch<LOGITS, false>(ta, tb, w, tiles, num_sms, stream);
+    if (a.lm.cap > 0.f)
+        return a.e ? launch<LOGITS, true, true>(ta, tb, w, tiles, num_sms, stream)
+                   : launch<LOGITS, false, true>(ta, tb, w, tiles, num_sms, stream);
+    return a.e ? launch<LOGITS, true, false>(ta, tb, w, tiles, num_sms, stream)
+               : launch<LOGITS, false, false>(ta, tb, w, tiles, num_sms, stream);
 }
 
 cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int splits, int num_sms,
@@ -562,7 +579,7 @@ cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile)), splits};
-    return launch<DH, false>(ta, tb, w, up(a.rows, kTile) * w.n_nt * splits, num_sms, stream);
+    return launch<DH>(ta, tb, w, up(a.rows, kTile) * w.n_nt * splits, num_sms, stream);
 }
 
 cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
@@ -570,7 +587,7 @@ cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile)), 1};
-    return launch<DW, false>(ta, tb, w, up(a.V, kTile) * w.n_nt, num_sms, stream);
+    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, num_sms, stream);
 }
 
 }  // namespace df2
