@@ -35,11 +35,11 @@ struct Plan {
     int64_t rows;        // of a piece
     int64_t pieces;
     int64_t e_rows, e_ld;
-    int n_stats, splits;
+    int n_stats;
     size_t count, map, targets, target_logit, h, stats, e, part, sums, bytes;
 };
 
-Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
+Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
     Plan p{};
     const bool grads = dh || dw;
     p.h_rows = up(P, 64);
@@ -52,7 +52,6 @@ Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
     p.rows = up((P + p.pieces - 1) / p.pieces, 256);
     if (p.rows > P) p.rows = P;
     p.e_rows = up(p.rows, 64);
-    p.splits = dh ? df2::loss_dh_splits(p.rows, D, V, num_sms) : 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -66,7 +65,9 @@ Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
     p.h = take(size_t(p.h_rows) * D * 2);
     p.stats = take(size_t(p.rows) * p.n_stats * 8);
     p.e = take(grads ? size_t(p.e_rows) * p.e_ld * 2 : 0);
-    p.part = take(p.splits > 1 ? size_t(p.splits) * p.rows * D * 4 : 0);
+    const int64_t splits = dh ? df2::loss_split_limit((V + 63) / 64) : 1;
+    const int64_t partial = splits > 1 ? splits * p.rows * D : 0;
+    p.part = take(size_t(partial < df2::kLossPartial ? partial : df2::kLossPartial) * 4);
     p.sums = take(dw && p.pieces > 1 ? size_t(V) * D * 4 : 0);
     p.bytes = at;
     return p;
@@ -150,9 +151,10 @@ cudaError_t run(const Call& c, const Plan& p, int num_sms) {
             g.out = c.dh;
             g.out_bf16 = rows.dh_bf16;
             g.part = reinterpret_cast<float*>(c.ws + p.part);
-            g.part_rows = p.rows;
-            e = df2::loss_dh_launch(g, p.e_rows, c.W, p.splits, num_sms, c.stream);
-            if (e == cudaSuccess && p.splits > 1) e = df2::loss_sum_parts_launch(g, p.splits, c.stream);
+            df2::LossDhGrid grid{};
+            e = df2::loss_dh_launch(g, p.e_rows, c.W, num_sms, &grid, c.stream);
+            if (e == cudaSuccess && df2::loss_split_limit((c.V + 63) / 64) > 1)
+                e = df2::loss_sum_parts_launch(g, grid, c.stream);
             if (e != cudaSuccess) break;
         }
         if (c.dw) {
@@ -199,7 +201,7 @@ int call(Call c, float multiplier, float cap, void* workspace, size_t workspace_
     }
     const int sms = num_sms_current();
     if (sms < 2) return DF2_ERR_CUDA;
-    const Plan p = make_plan(c.P, c.D, c.V, c.dh, c.dw, sms);
+    const Plan p = make_plan(c.P, c.D, c.V, c.dh, c.dw);
     if (workspace_bytes < p.bytes || !workspace) return DF2_ERR_WORKSPACE_TOO_SMALL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return DF2_ERR_UNSUPPORTED;
     c.ws = static_cast<char*>(workspace);
@@ -208,8 +210,7 @@ int call(Call c, float multiplier, float cap, void* workspace, size_t workspace_
 
 size_t workspace_size(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
     if (check_shape(P, D, V) != DF2_OK || P == 0) return 0;
-    const int sms = num_sms_current();
-    return make_plan(P, D, V, dh, dw, sms < 2 ? 152 : sms).bytes;
+    return make_plan(P, D, V, dh, dw).bytes;
 }
 
 }  // namespace

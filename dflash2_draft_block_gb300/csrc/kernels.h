@@ -180,22 +180,56 @@ struct LossGemmArgs {
     LogitMap lm;
     uint16_t* e;              // [rows, e_ld], nullable
     int64_t e_ld;
-    // the gradients: dh rows by map, or their parts [splits, part_rows, D]; dW
+    // the gradients: dh rows by map, or their parts [splits, live rows, D]; dW
     void* out;
     bool out_bf16;
     float* part;
-    int64_t part_rows;
     float* sums;              // [V, D] between the pieces of one call, nullable where there is one
     bool first, last, accumulate;
 };
-int loss_dh_splits(int64_t rows, int64_t D, int64_t V, int num_sms);
+
+// How many ways dh's product is split along V, for `tiles` tiles of `steps` steps (of 64) on
+// `units` clusters: the busiest cluster's steps at 0.3 us, and the partial sums' way out and
+// back at 4 TB/s, in ns.  The live rows decide, so it is worked out on the device, by each
+// kernel that needs it; in whole numbers, so that all find the same.
+constexpr int kLossSplits = 64;
+constexpr int64_t kLossPartial = int64_t(1) << 27;  // fp32 sums held at most
+__host__ __device__ inline int loss_split_limit(int64_t steps) {
+    const int64_t s = (steps + 15) / 16;
+    return int(s < kLossSplits ? s : kLossSplits);
+}
+// By a whole warp.
+__device__ __forceinline__ int loss_splits(int64_t tiles, int64_t steps, int64_t units, int64_t rows, int64_t D, int lane) {
+    const int limit = loss_split_limit(steps);
+    int64_t best = INT64_MAX;
+    for (int s = lane + 1; s <= limit && (s == 1 || s * rows * D <= kLossPartial); s += 32) {
+        int64_t ns = (tiles * s + units - 1) / units * ((steps + s - 1) / s) * 300;
+        if (s > 1) ns += 3000 + s * rows * D * 2 / 1000;
+        const int64_t key = ns * 128 + s;  // equal times: the fewer
+        best = key < best ? key : best;
+    }
+    for (int o = 16; o; o >>= 1) {
+        const int64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
+        best = other < best ? other : best;
+    }
+    return int(best & 127);
+}
+// Tiles of clusters: `across` by `shared`; quads take the shared index by twos, and where it is
+// odd the last of it with the other index by twos.
+__host__ __device__ inline int loss_cluster_tiles(int across, int shared, bool quad) {
+    return quad ? across * (shared / 2) + (shared & 1) * ((across + 1) / 2) : across * shared;
+}
+struct LossDhGrid {
+    int n_nt, units;          // N tiles, clusters
+    bool quad;
+};
 cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t h_rows, const uint16_t* W, int num_sms,
                                cudaStream_t stream);
-cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int splits, int num_sms,
+cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int num_sms, LossDhGrid* grid,
                            cudaStream_t stream);
 cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
                            cudaStream_t stream);
-cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, int splits, cudaStream_t stream);
+cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, const LossDhGrid& grid, cudaStream_t stream);
 
 struct LossRowArgs {
     const int32_t* count;

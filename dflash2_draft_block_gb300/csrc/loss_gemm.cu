@@ -22,6 +22,8 @@
 // dealt round-robin to the pairs.  Rows without a target were left out beforehand, so the
 // number of rows is read from the device.  All waits are bounded.
 #include <cudaTypedefs.h>
+#include <cstdio>
+#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -40,10 +42,7 @@ constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
 constexpr int kStages = 7;
 constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
-#ifndef KG
-#define KG 16
-#endif
-constexpr int kGroup = KG;                      // M units that share a pass over W
+constexpr int kGroup = 16;                     // M units that share a pass over W (8: 3% slower; 32: 2%)
 constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
 constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
 
@@ -51,7 +50,7 @@ enum { LOGITS, DH, DW };
 
 struct Work {
     LossGemmArgs a;
-    int n_nt, splits;
+    int n_nt;
 };
 
 // K-major as tc::sw128_kmajor_desc; MN-major: panels kStep * 128 bytes apart.
@@ -256,8 +255,12 @@ __device__ __forceinline__ void write_row(float (&x)[128], int n, const float* a
     }
 }
 
-template <int MODE, bool E, bool CAP>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+// QUAD: a cluster of two pairs on neighbouring tiles that share an operand (LOGITS: two M units
+// and W's rows; the gradients: two N tiles and g's): the first pair's CTAs load it for the CTA
+// of the same rank in the other pair too, and a stage is free when both pairs' MMAs have read
+// it.  A tile past the end is computed on zeros and not written.
+template <int MODE, bool E, bool CAP, bool QUAD>
+__global__ void __launch_bounds__(kThreads, 1)
 loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const __grid_constant__ Work w) {
     constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
@@ -273,13 +276,15 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = int(tc::cluster_ctarank());
+    const uint32_t crank = tc::cluster_ctarank(), lead = crank & ~1u;  // in the cluster; its pair's leader
+    const int rank = int(crank & 1), which = int(crank >> 1);          // in the pair; which pair
     const bool leader = rank == 0;
+    constexpr int kPairs = QUAD ? 2 : 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(&full[s], 1);
-            tc::mbar_init(&empty[s], 1);
+            tc::mbar_init(&empty[s], kPairs);
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&tfull[b], 1);
@@ -307,30 +312,50 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const int64_t left = int64_t(*a.count) - a.row0;
     const int live = left < 0 ? 0 : left > a.rows ? a.rows : int(left);
     const int n_mu = (int(MODE == DW ? a.V : live) + kTile - 1) / kTile;
-    const int total = n_mu * w.n_nt * w.splits;
     const int k_total = (int(MODE == LOGITS ? a.D : MODE == DH ? a.V : live) + kStep - 1) / kStep;
-    const int units = int(gridDim.x) >> 1, unit = int(blockIdx.x) >> 1;
+    const int units = int(gridDim.x) / (2 * kPairs), unit = int(blockIdx.x) / (2 * kPairs);
+    const int n_nt = w.n_nt;
+    const int tiles = MODE == LOGITS ? loss_cluster_tiles(n_nt, n_mu, QUAD) : loss_cluster_tiles(n_mu, n_nt, QUAD);
+    const int splits = MODE == DH ? loss_splits(tiles, k_total, units, live, a.D, lane) : 1;
+    const int total = tiles * splits;
 
-    // tile i: its M unit, N tile and stages [k0, k1)
+    // tile i: its M unit, N tile and stages [k0, k1).  alone: the pairs of a cluster share
+    // nothing (the odd M unit or N tile at the end, whose other index they take by twos).
     struct Tile {
         int mu, nt, split, k0, k1;
+        bool alone;
     };
     auto tile = [&](int i) {
         Tile t;
+        t.split = i / tiles;
+        const int j = i - t.split * tiles;
+        t.alone = false;
         if (MODE == LOGITS) {  // M fastest in groups: W streams past, a group's rows of h stay in L2
-            const int group = i / (kGroup * w.n_nt), first = group * kGroup;
-            const int wide = min(kGroup, n_mu - first), rest = i - first * w.n_nt;
-            t.mu = first + rest % wide;
-            t.nt = rest / wide;
-            t.split = 0;
-        } else {               // N fastest: the pairs of a moment share g's rows
-            t.nt = i % w.n_nt;
-            const int rest = i / w.n_nt;
-            t.mu = rest % n_mu;
-            t.split = rest / n_mu;
+            constexpr int kRun = kGroup / kPairs;
+            const int n_m = n_mu / kPairs, odd = j - n_m * n_nt;
+            if (odd < 0) {
+                const int first = j / (kRun * n_nt) * kRun;
+                const int wide = min(kRun, n_m - first), rest = j - first * n_nt;
+                t.mu = (first + rest % wide) * kPairs + which;
+                t.nt = rest / wide;
+            } else {
+                t.mu = n_mu - 1;
+                t.nt = odd * 2 + which;
+                t.alone = true;
+            }
+        } else {               // N fastest: the clusters of a moment share g's rows
+            const int n_n = n_nt / kPairs, odd = j - n_mu * n_n;
+            if (odd < 0) {
+                t.nt = j % n_n * kPairs + which;
+                t.mu = j / n_n;
+            } else {
+                t.nt = n_nt - 1;
+                t.mu = odd * 2 + which;
+                t.alone = true;
+            }
         }
-        t.k0 = int(int64_t(k_total) * t.split / w.splits);
-        t.k1 = int(int64_t(k_total) * (t.split + 1) / w.splits);
+        t.k0 = int(int64_t(k_total) * t.split / splits);
+        t.k1 = int(int64_t(k_total) * (t.split + 1) / splits);
         return t;
     };
 
@@ -356,21 +381,30 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     if (leader) tc::mbar_arrive_expect_tx(&full[stage], 4 * kOperand);
                     uint8_t* da = smem + size_t(stage) * 2 * kOperand;
                     uint8_t* db = da + kOperand;
-                    const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), 0);
+                    const uint32_t fb = tc::mapa_shared(tc::smem_u32(&full[stage]), lead);
                     const int ma = t.mu * kTile + rank * 128, nb = t.nt * kTile + rank * 128;
+                    // the operand that a cluster shares is loaded once, by its first pair
+                    const uint16_t both = uint16_t((1u << crank) | (1u << (crank + 2)));
+                    auto own = [&](uint8_t* to, const CUtensorMap* map, int x, int y, uint64_t policy) {
+                        tc::tma_load_2d_pair(to, map, fb, x, y, policy);
+                    };
+                    auto shared = [&](uint8_t* to, const CUtensorMap* map, int x, int y, uint64_t policy) {
+                        if (!QUAD || t.alone) tc::tma_load_2d_pair(to, map, fb, x, y, policy);
+                        else if (which == 0) tc::tma_load_2d_pair_mc(to, map, fb, both, x, y, policy);
+                    };
                     if (MODE == LOGITS) {
-                        tc::tma_load_2d_pair(da, &tm_a, fb, k * kStep, int(a.row0) + ma, pol_a);
-                        tc::tma_load_2d_pair(db, &tm_b, fb, k * kStep, nb, pol_b);
+                        own(da, &tm_a, k * kStep, int(a.row0) + ma, pol_a);
+                        shared(db, &tm_b, k * kStep, nb, pol_b);
                     } else {
                         if (A_MN) {
-                            tc::tma_load_2d_pair(da, &tm_a, fb, ma, k * kStep, pol_a);
-                            tc::tma_load_2d_pair(da + kOperand / 2, &tm_a, fb, ma + 64, k * kStep, pol_a);
+                            shared(da, &tm_a, ma, k * kStep, pol_a);
+                            shared(da + kOperand / 2, &tm_a, ma + 64, k * kStep, pol_a);
                         } else {
-                            tc::tma_load_2d_pair(da, &tm_a, fb, k * kStep, ma, pol_a);
+                            shared(da, &tm_a, k * kStep, ma, pol_a);
                         }
                         const int kb = k * kStep + (MODE == DW ? int(a.row0) : 0);
-                        tc::tma_load_2d_pair(db, &tm_b, fb, nb, kb, pol_b);
-                        tc::tma_load_2d_pair(db + kOperand / 2, &tm_b, fb, nb + 64, kb, pol_b);
+                        own(db, &tm_b, nb, kb, pol_b);
+                        own(db + kOperand / 2, &tm_b, nb + 64, kb, pol_b);
                     }
                     armed[stage] = int8_t(phase);
                     if (++stage == kStages) {
@@ -380,8 +414,8 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
             }
             if (!ok && leader) {
-                // wait (bounded) for the copies in flight; CTA 1's complete on CTA 0's barriers
-                // too, and it leaves only after the closing cluster barrier
+                // wait (bounded) for the copies in flight; the pair's other CTA's complete on these
+                // barriers too, and it leaves only after the closing cluster barrier
                 volatile int never = 0;
                 for (int s = 0; s < kStages; ++s)
                     if (armed[s] >= 0) tc::mbar_wait(&full[s], uint32_t(armed[s]), &never);
@@ -416,18 +450,18 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                             tc::mma_bf16_pair(d, operand_desc(sa + q * (A_MN ? 2048 : 32), A_MN),
                                               operand_desc(sb + q * (B_MN ? 2048 : 32), B_MN), idesc,
                                               (kk != k || q != 0) ? 1u : 0u);
-                        tc::mma_commit_pair(&empty[stage], 0x3);
+                        tc::mma_commit_pair(&empty[stage], QUAD ? 0xF : 0x3);
                         if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1;
                         }
                     }
-                    if (ok) tc::mma_commit_pair(&tfull[buf], 0x3);
+                    if (ok) tc::mma_commit_pair(&tfull[buf], uint16_t(0x3u << lead));
                     buf ^= 1;
                     if (buf == 0) tphase ^= 1;
                 }
             }
-            tc::mma_commit_pair(mma_done, 0x3);
+            tc::mma_commit_pair(mma_done, uint16_t(0x3u << lead));
             volatile int never = 0;
             tc::mbar_wait(mma_done, 0, &never);
         }
@@ -458,21 +492,21 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), 0));
+                if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
                 buf ^= 1;
                 if (buf == 0) tphase ^= 1;
             }
             if (!ok) break;
             const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
             if (MODE == LOGITS) {
-                if (m < live) logits_epilogue<E, CAP>(a, x, m, t.nt, half);
+                if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, half);
             } else {
                 const int n0 = t.nt * kTile + half * 128;
                 const int n = min(128, int(a.D) - n0);
                 if (MODE == DH) {
                     if (m < live && n > 0) {
-                        if (w.splits > 1) {
-                            float* part = a.part + (int64_t(t.split) * a.part_rows + m) * a.D + n0;
+                        if (splits > 1) {
+                            float* part = a.part + (int64_t(t.split) * live + m) * a.D + n0;
                             write_row(x, n, nullptr, nullptr, part, false);
                         } else {
                             const int64_t o = int64_t(a.map[a.row0 + m]) * a.D + n0;
@@ -496,8 +530,8 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
     tc::fence_before_sync();
     __syncthreads();
-    // CTA 0's MMAs read this CTA's shared memory and write its TMEM: neither CTA frees TMEM or
-    // exits before both are done
+    // a pair's MMAs read both CTAs' shared memory and write their TMEM, and copies go to every
+    // CTA of a cluster: none frees TMEM or exits before all are done
     tc::cluster_sync_all();
     if (threadIdx.x == 0 && *abort_flag && a.status) atomicOr(a.status, DF2_STATUS_WAIT_TIMEOUT);
     if (warp == 1) {
@@ -529,65 +563,109 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int MODE, bool E = false, bool CAP = false>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, int num_sms,
-                   cudaStream_t stream) {
-    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E, CAP>>(kSmem);
+template <int MODE, bool E, bool CAP, bool QUAD>
+cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, int64_t clusters,
+                            cudaStream_t stream) {
+    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E, CAP, QUAD>>(kSmem);
     if (e != cudaSuccess) return e;
-    const int64_t pairs = num_sms / 2 < tiles ? num_sms / 2 : tiles;
-    loss_gemm_kernel<MODE, E, CAP><<<unsigned(2 * pairs), kThreads, kSmem, stream>>>(ta, tb, w);
+    constexpr unsigned kCtas = QUAD ? 4 : 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCtas * unsigned(clusters < tiles ? clusters : tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     note_launch();
-    return cudaGetLastError();
+    return cudaLaunchKernelEx(&cfg, loss_gemm_kernel<MODE, E, CAP, QUAD>, ta, tb, w);
+}
+
+// Clusters of two pairs (four SMs of one GPC) that run at once on the current device, asked
+// once; 0 where the question fails.
+template <int MODE, bool E, bool CAP>
+int quad_slots() {
+    constexpr int kDevices = 64;
+    static std::mutex mu;
+    static int known[kDevices];  // plus one
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev] == 0) {
+        if (allow_smem<loss_gemm_kernel<MODE, E, CAP, true>>(kSmem) != cudaSuccess) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(4);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 4;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, loss_gemm_kernel<MODE, E, CAP, true>, &cfg) != cudaSuccess) n = 0;
+        known[dev] = n + 1;
+    }
+    return known[dev] - 1;
+}
+
+template <int MODE, bool E = false, bool CAP = false>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, bool quad, int num_sms,
+                   cudaStream_t stream) {
+    if (quad) {
+        const int slots = quad_slots<MODE, E, CAP>();
+        if (slots > 0) return launch_clusters<MODE, E, CAP, true>(ta, tb, w, slots, slots, stream);
+    }
+    return launch_clusters<MODE, E, CAP, false>(ta, tb, w, tiles, num_sms / 2, stream);
 }
 
 int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
 
 }  // namespace
 
-int loss_dh_splits(int64_t rows, int64_t D, int64_t V, int num_sms) {
-    // the time of the busiest pair (a stage takes 0.3 us) and of writing and reading the
-    // partial sums at 4 TB/s
-    const int64_t tiles = up(rows, kTile) * up(D, kTile), steps = up(V, kStep), pairs = num_sms / 2;
-    int best = 1;
-    double least = 0.0;
-    for (int s = 1; s <= 64 && s <= up(steps, kSegment); ++s) {
-        double us = double(up(tiles * s, pairs)) * double(up(steps, s)) * 0.3;
-        if (s > 1) us += 3.0 + double(s) * double(rows) * double(D) * 8.0 / 4e6;
-        if (s == 1 || us < least) {
-            least = us;
-            best = s;
-        }
-    }
-    return best;
-}
-
 cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t h_rows, const uint16_t* W, int num_sms,
                                cudaStream_t stream) {
     CUtensorMap ta, tb;
     if (!make_map(&ta, h, h_rows, a.D, a.D, 128) || !make_map(&tb, W, a.V, a.D, a.D, 128)) return cudaErrorInvalidValue;
-    const Work w{a, int(up(a.V, kTile)), 1};
+    const Work w{a, int(up(a.V, kTile))};
     const int64_t tiles = up(a.rows, kTile) * w.n_nt;
+    bool quad = a.rows > kTile;
+    if (getenv("LG_LO")) quad = quad && atoi(getenv("LG_LO"));
     if (a.lm.cap > 0.f)
-        return a.e ? launch<LOGITS, true, true>(ta, tb, w, tiles, num_sms, stream)
-                   : launch<LOGITS, false, true>(ta, tb, w, tiles, num_sms, stream);
-    return a.e ? launch<LOGITS, true, false>(ta, tb, w, tiles, num_sms, stream)
-               : launch<LOGITS, false, false>(ta, tb, w, tiles, num_sms, stream);
+        return a.e ? launch<LOGITS, true, true>(ta, tb, w, tiles, quad, num_sms, stream)
+                   : launch<LOGITS, false, true>(ta, tb, w, tiles, quad, num_sms, stream);
+    return a.e ? launch<LOGITS, true, false>(ta, tb, w, tiles, quad, num_sms, stream)
+               : launch<LOGITS, false, false>(ta, tb, w, tiles, quad, num_sms, stream);
 }
 
-cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int splits, int num_sms,
+cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int num_sms, LossDhGrid* grid,
                            cudaStream_t stream) {
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
-    const Work w{a, int(up(a.D, kTile)), splits};
-    return launch<DH>(ta, tb, w, up(a.rows, kTile) * w.n_nt * splits, num_sms, stream);
+    const Work w{a, int(up(a.D, kTile))};
+    bool quad = w.n_nt > 1;
+    if (getenv("LG_DH")) quad = quad && atoi(getenv("LG_DH"));
+    const int slots = quad ? quad_slots<DH, false, false>() : 0;
+    quad = slots > 0;
+    *grid = {w.n_nt, quad ? slots : num_sms / 2, quad};
+    // every cluster that fits: the splits share the rows that turn out to be live among them
+    return quad ? launch_clusters<DH, false, false, true>(ta, tb, w, slots, slots, stream)
+                : launch_clusters<DH, false, false, false>(ta, tb, w, num_sms / 2, num_sms / 2, stream);
 }
 
 cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
                            cudaStream_t stream) {
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
-    const Work w{a, int(up(a.D, kTile)), 1};
-    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, num_sms, stream);
+    const Work w{a, int(up(a.D, kTile))};
+    bool quad = w.n_nt > 1;
+    if (getenv("LG_DW")) quad = quad && atoi(getenv("LG_DW"));
+    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, quad, num_sms, stream);
 }
 
 }  // namespace df2

@@ -140,33 +140,58 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
     const float gt = -sum * w * (1.f - bent * bent);
     const int64_t t = a.live_targets[a.row0 + row];
     uint16_t* e = a.e + row * a.e_ld;
-    for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += kThreads * 8) {
-        float f[8];
-        unpack8_f16(*reinterpret_cast<const uint4*>(e + c), f);
-        const float2 s = stats[c / 128];
-        const float by = s.x == -INFINITY ? w_e : w_e * exp2f((s.x - top) * kLog2e);
+    constexpr int kAhead = 4;  // units of a thread that are loaded together
+    for (int64_t c = c0 + threadIdx.x * 8; c < c1; c += kAhead * kThreads * 8) {
+        uint4 in[kAhead];
+        float m[kAhead];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = c + j == t ? gt : f[j] * by;
-        *reinterpret_cast<uint4*>(e + c) =
-            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = c + k * kThreads * 8;
+            if (at < c1) {
+                in[k] = __ldcs(reinterpret_cast<const uint4*>(e + at));
+                m[k] = __ldg(&stats[at / 128].x);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t at = c + k * kThreads * 8;
+            if (at >= c1) break;
+            float f[8];
+            unpack8_f16(in[k], f);
+            const float by = m[k] == -INFINITY ? w_e : w_e * exp2f((m[k] - top) * kLog2e);
+            const int64_t hit = t - at;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = j == hit ? gt : f[j] * by;
+            *reinterpret_cast<uint4*>(e + at) =
+                make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        }
     }
 }
 
 // A thread sums 4 columns of a row.
 __global__ void __launch_bounds__(kThreads)
-sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* map, const float* part, int splits,
-                 int64_t part_rows, int64_t D, void* dh, bool bf16) {
+sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* map, const float* part, int64_t V,
+                 int64_t D, LossDhGrid grid, void* dh, bool bf16) {
+    __shared__ int shared_splits;
     const int64_t left = int64_t(*count) - row0;
     const int64_t live = left < 0 ? 0 : left > rows ? rows : left;
     const int64_t row = blockIdx.x;
     if (row >= live) return;
+    if (threadIdx.x < 32) {
+        const int tiles = loss_cluster_tiles(int((live + 255) / 256), grid.n_nt, grid.quad);
+        const int splits = loss_splits(tiles, (V + 63) / 64, grid.units, live, D, threadIdx.x);
+        if (threadIdx.x == 0) shared_splits = splits;
+    }
+    __syncthreads();
+    const int splits = shared_splits;
+    if (splits == 1) return;  // the product wrote dh itself
     const int64_t p = map[row0 + row];
     for (int64_t d = 4 * (int64_t(blockIdx.y) * kThreads + threadIdx.x); d < D; d += 4 * int64_t(gridDim.y) * kThreads) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
         const float* from = part + row * D + d;
 #pragma unroll 4
         for (int k = 0; k < splits; ++k) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * part_rows * D));
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * live * D));
             s.x += v.x;
             s.y += v.y;
             s.z += v.z;
@@ -208,10 +233,10 @@ cudaError_t loss_row_launch(const LossRowArgs& a, int64_t e_rows, int num_sms, c
     return cudaGetLastError();
 }
 
-cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, int splits, cudaStream_t stream) {
+cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, const LossDhGrid& grid, cudaStream_t stream) {
     const int64_t across = (a.D + 4 * kThreads - 1) / (4 * kThreads);
     sum_parts_kernel<<<dim3(unsigned(a.rows), unsigned(across < 64 ? across : 64)), kThreads, 0, stream>>>(
-        a.count, a.row0, a.rows, a.map, a.part, splits, a.part_rows, a.D, a.out, a.out_bf16);
+        a.count, a.row0, a.rows, a.map, a.part, a.V, a.D, grid, a.out, a.out_bf16);
     note_launch();
     return cudaGetLastError();
 }
