@@ -43,7 +43,7 @@ Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
     Plan p{};
     const bool grads = dh || dw;
     p.h_rows = up(P, 64);
-    p.n_stats = int(up(V, 256) / 128);
+    p.n_stats = int(up(V, 256) / df2::kLossStats);
     p.e_ld = up(V, 256);
     const int64_t row_bytes = grads ? p.e_ld * 2 : int64_t(p.n_stats) * 8;
     int64_t most = (grads ? kPieceBytes : kPieceStats) / row_bytes / 256 * 256;

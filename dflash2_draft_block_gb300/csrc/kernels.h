@@ -164,6 +164,7 @@ struct LossRowsArgs {
 };
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream);
 
+constexpr int kLossStats = 64;          // columns that share a maximum
 constexpr float kExpScale = 32768.f;  // exp(x - M) is held in fp16 in units of 2^-15
 struct LossGemmArgs {
     const int32_t* count;
@@ -175,7 +176,7 @@ struct LossGemmArgs {
     // logits
     const int32_t* targets;   // live_targets
     float* target_logit;      // [P], of the live rows
-    float2* stats;            // [rows, n_stats]: (M, sum of exp(x - M)) of 128 columns each
+    float2* stats;            // [rows, n_stats]: (M, sum of exp(x - M)) of kLossStats columns each
     int n_stats;
     LogitMap lm;
     uint16_t* e;              // [rows, e_ld], nullable

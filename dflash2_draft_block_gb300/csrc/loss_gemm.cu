@@ -1,6 +1,6 @@
 // The matrix products of the unary loss on the tensor cores, CTA pairs on 256 x 256 tiles
 // (tcgen05.mma.cta_group::2, bf16 in, fp32 sums), with three epilogues:
-//   LOGITS  u = h W^T, never stored: of each row's 128 columns the largest logit M and the sum
+//   LOGITS  u = h W^T, never stored: of each row's 64 columns the largest logit M and the sum
 //           of exp(u - M) over the columns other than the target's, and the target's logit.
 //           With `e`, also exp(u - M) itself (times the softcap's slope) as fp16.
 //   DH      dh = g W:    A = g (K-major: its rows run along K = V), B = W, MN-major
@@ -14,16 +14,14 @@
 // rounding it, so a sum of n steps drifts towards zero by about n / 4 ulp: a logit of 4096
 // products came out 4e-6 of itself too small, which a loss would show.  The MMAs
 // therefore sum kSegment K elements at a time into one of two TMEM accumulators while the
-// epilogue warps add the other to running sums in fp32 registers (128 columns a thread, eight
+// epilogue warps add the other to running sums in fp32 registers (64 columns a thread, sixteen
 // warps), rounded to nearest.
 //
-// Roles (384 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-11
-// are the epilogue (TMEM lane = row; two warps a quarter, 128 columns each).  Tiles are
+// Roles (640 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-19
+// are the epilogue (TMEM lane = row; four warps a quarter, 64 columns each).  Tiles are
 // dealt round-robin to the pairs.  Rows without a target were left out beforehand, so the
 // number of rows is read from the device.  All waits are bounded.
 #include <cudaTypedefs.h>
-#include <cstdio>
-#include <cstdlib>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -33,10 +31,11 @@
 namespace df2 {
 namespace {
 
-constexpr int kThreads = 384;
-// Registers: launched with 168 a thread; the first four warps keep 88 and the epilogue's eight
-// take 208 (128 * 88 + 256 * 208 = 384 * 168).
-constexpr int kRoleRegisters = 88, kEpilogueRegisters = 208;
+constexpr int kThreads = 640;
+// Registers: launched with 96 a thread; the first four warps keep 48 and the epilogue's sixteen
+// take 104 (128 * 48 + 512 * 104 <= 640 * 96).
+constexpr int kRoleRegisters = 48, kEpilogueRegisters = 104;
+constexpr int kCols = kLossStats;              // columns of an epilogue thread
 constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
@@ -87,17 +86,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return w;
 }
 
-// The x held by a thread moves 32 places towards the front, the first 32 to the back.  Four
-// times is once around: a loop over 32 columns at a time that keeps x in registers.  (All 128
-// columns unrolled were thousands of instructions, read anew for every tile: 10 us of it.)
-__device__ __forceinline__ void turn(float (&x)[128]) {
+// The two halves of the x held by a thread change places: a loop over 32 columns at a time that
+// keeps x in registers.  (All of a row's columns unrolled were thousands of instructions, read
+// anew for every tile.)
+__device__ __forceinline__ void turn(float (&x)[kCols]) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
         const float first = x[j];
         x[j] = x[j + 32];
-        x[j + 32] = x[j + 64];
-        x[j + 64] = x[j + 96];
-        x[j + 96] = first;
+        x[j + 32] = first;
     }
 }
 
@@ -134,21 +131,21 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&w)[8], bool wid
     }
 }
 
-// One row's 128 logits of a tile (x, raw): the statistics, and e where asked, in fp16 in
+// One row's 64 logits of a tile (x, raw): the statistics, and e where asked, in fp16 in
 // units of 2^-15 (11 bits of exp(x - M) down to M - 20, then fewer until M - 27; bf16 here and
 // again as g would double the factors' rounding error).
 template <bool E, bool CAP>
-__device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[128], int row, int nt, int half) {
-    const int64_t c0 = int64_t(nt) * kTile + half * 128;
+__device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[kCols], int row, int nt, int part) {
+    const int64_t c0 = int64_t(nt) * kTile + part * kCols;
     const int64_t t = a.targets[a.row0 + row] - c0;
     const float cap = a.lm.cap, mul = CAP ? a.lm.mul / cap : a.lm.mul;
     // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
     auto map = [&](float u) { return CAP ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
-    if ((t >= 0 && t < 128) || c0 + 128 > a.V) {  // the target and what is no column are left out
-        const int end = c0 + 128 > a.V ? int(a.V - c0) : 128;
+    if ((t >= 0 && t < kCols) || c0 + kCols > a.V) {  // the target and what is no column are left out
+        const int end = c0 + kCols > a.V ? int(a.V - c0) : kCols;
         float xt = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < kCols; c += 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
                 if (c + j == t) xt = x[j];
@@ -156,11 +153,11 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
             }
             turn(x);
         }
-        if (t >= 0 && t < 128) a.target_logit[a.row0 + row] = map(xt);
+        if (t >= 0 && t < kCols) a.target_logit[a.row0 + row] = map(xt);
     }
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 128; ++j) top = fmaxf(top, x[j]);
+    for (int j = 0; j < kCols; ++j) top = fmaxf(top, x[j]);
     const bool none = top == -INFINITY;
     // x - M in the units of the logits as they are mapped: without a cap the multiplier waits
     const float base = none ? 0.f : CAP ? map(top) : top;
@@ -169,7 +166,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
 #pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
+    for (int c = 0; c < kCols; c += 32) {
 #pragma unroll
         for (int j0 = 0; j0 < 32; j0 += 16) {
             uint32_t word[8];
@@ -191,64 +188,64 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
         }
         turn(x);
     }
-    a.stats[int64_t(row) * a.n_stats + nt * 2 + half] =
+    a.stats[int64_t(row) * a.n_stats + nt * (kTile / kCols) + part] =
         make_float2(none ? top : CAP ? base : __fmul_rn(top, mul), (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
-// One row's columns [0, n) (n a multiple of 8) of sums to `out`, plus what is added to.
-__device__ __forceinline__ void write_row(float (&x)[128], int n, const float* add32, const void* add, void* out, bool b16) {
+// x += the columns [0, n) (n a multiple of 8) at p, 16 at a time: their loads are waited for once.
+template <bool B16>
+__device__ __forceinline__ void add_row(float (&x)[kCols], int n, const void* p) {
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += 32) {
+#pragma unroll
+        for (int s = 0; s < 32; s += 16) {
+            constexpr int kLoads = B16 ? 2 : 4, kEach = 16 / kLoads;
+            const char* at = static_cast<const char*>(p) + (c + s) * (B16 ? 2 : 4);
+            uint4 f[kLoads];
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                f[j] = c + s + kEach * j < n ? reinterpret_cast<const uint4*>(at)[j] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (B16) {
+                        x[s + 8 * j + 2 * k] += bf16_lo(w[k]);
+                        x[s + 8 * j + 2 * k + 1] += bf16_hi(w[k]);
+                    } else {
+                        x[s + 4 * j + k] += __uint_as_float(w[k]);
+                    }
+                }
+            }
+        }
+        turn(x);
+    }
+}
+
+// One row's columns [0, n) (n a multiple of 8) to `out`.
+template <bool B16>
+__device__ __forceinline__ void write_row(float (&x)[kCols], int n, void* out) {
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll 1
-    for (int c = 0; c < n; c += 32) {
-        // the loads first, so that the loop waits once for all of them
-        uint4 f[8], g[8];
-        const int pieces = b16 ? 4 : 8;  // of 16 bytes
+    for (int c = 0; c < kCols; c += 32) {
+        char* to = static_cast<char*>(out) + c * (B16 ? 2 : 4);
+        if (B16) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            f[j] = add32 && c + 4 * j < n ? reinterpret_cast<const uint4*>(add32 + c)[j] : make_uint4(0u, 0u, 0u, 0u);
-            g[j] = add && j < pieces && c + (32 / pieces) * j < n
-                       ? reinterpret_cast<const uint4*>(static_cast<const char*>(add) + c * (b16 ? 2 : 4))[j]
-                       : make_uint4(0u, 0u, 0u, 0u);
-        }
+            for (int s = 0; s < 32; s += 16) {
+                uint32_t w[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[4 * j + k] += __uint_as_float(w[k]);
-        }
-        if (b16) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float o[8];
-                unpack8(g[j], o);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[8 * j + k] += o[k];
+                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[s + 2 * j], x[s + 2 * j + 1]);
+                if (c + s + 16 <= n) store8(to + 2 * s, w, wide);
+                else if (c + s < n) *reinterpret_cast<uint4*>(to + 2 * s) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t w[4] = {g[j].x, g[j].y, g[j].z, g[j].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) x[4 * j + k] += __uint_as_float(w[k]);
-            }
-        }
-        if (b16) {
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 16) {
+            for (int s = 0; s < 32; s += 8) {
                 uint32_t w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[j0 + 2 * j], x[j0 + 2 * j + 1]);
-                uint16_t* to = static_cast<uint16_t*>(out) + c + j0;
-                if (c + j0 + 16 <= n) store8(to, w, wide);
-                else if (c + j0 < n) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-#pragma unroll
-            for (int j0 = 0; j0 < 32; j0 += 8) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[j0 + j]);
-                if (c + j0 < n) store8(static_cast<float*>(out) + c + j0, w, wide);
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[s + j]);
+                if (c + s < n) store8(to + 4 * s, w, wide);
             }
         }
         turn(x);
@@ -288,7 +285,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&tfull[b], 1);
-            tc::mbar_init(&tempty[b], 16);  // the epilogue warps of both CTAs
+            tc::mbar_init(&tempty[b], 32);  // the epilogue warps of both CTAs
         }
         tc::mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -307,6 +304,8 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     tc::cluster_sync_all();
     tc::fence_after_sync();
     const uint32_t tmem_base = *tmem_holder;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // what is above may overlap the kernel before
 
     // the rows of this piece that have a target
     const int64_t left = int64_t(*a.count) - a.row0;
@@ -468,23 +467,34 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     } else {
         // ---------------------------------------------------------- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegisters));
-        const int quarter = warp & 3, half = (warp >> 2) - 1;
+        const int quarter = warp & 3, part = (warp >> 2) - 1;
         int buf = 0;
         uint32_t tphase = 0;
         bool ok = true;
         for (int i = unit; i < total && ok; i += units) {
             const Tile t = tile(i);
-            float x[128];
+            const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
+            if (MODE == DW && a.last && a.accumulate && m < a.V) {
+                // what dW holds is on its way while the product is summed
+                const int n0 = t.nt * kTile + part * kCols;
+                if (n0 < a.D) {
+                    const int64_t size = a.out_bf16 ? 2 : 4;
+                    const char* p = static_cast<const char*>(a.out) + (int64_t(m) * a.D + n0) * size;
+                    for (int64_t o = 0; o < kCols * size && n0 + o / size < a.D; o += 128)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + o));
+                }
+            }
+            float x[kCols];
 #pragma unroll
-            for (int j = 0; j < 128; ++j) x[j] = 0.f;
+            for (int j = 0; j < kCols; ++j) x[j] = 0.f;
             for (int k = t.k0; k < t.k1; k += kSegment) {
                 ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
                 if (!ok) break;
                 tc::fence_after_sync();
                 const uint32_t taddr =
-                    tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + half * 128);
+                    tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + part * kCols);
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < kCols; c += 32) {
                     float v[32];
                     tmem_ld32(taddr + c, v);
 #pragma unroll
@@ -497,31 +507,35 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 if (buf == 0) tphase ^= 1;
             }
             if (!ok) break;
-            const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
             if (MODE == LOGITS) {
-                if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, half);
+                if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, part);
             } else {
-                const int n0 = t.nt * kTile + half * 128;
-                const int n = min(128, int(a.D) - n0);
+                const int n0 = t.nt * kTile + part * kCols;
+                const int n = min(kCols, int(a.D) - n0);
+                if (n <= 0) continue;
                 if (MODE == DH) {
-                    if (m < live && n > 0) {
+                    if (m < live) {
                         if (splits > 1) {
-                            float* part = a.part + (int64_t(t.split) * live + m) * a.D + n0;
-                            write_row(x, n, nullptr, nullptr, part, false);
+                            write_row<false>(x, n, a.part + (int64_t(t.split) * live + m) * a.D + n0);
                         } else {
                             const int64_t o = int64_t(a.map[a.row0 + m]) * a.D + n0;
-                            write_row(x, n, nullptr, nullptr, static_cast<char*>(a.out) + o * (a.out_bf16 ? 2 : 4),
-                                      a.out_bf16);
+                            if (a.out_bf16) write_row<true>(x, n, static_cast<uint16_t*>(a.out) + o);
+                            else write_row<false>(x, n, static_cast<float*>(a.out) + o);
                         }
                     }
-                } else if (m < a.V && n > 0) {
+                } else if (m < a.V) {
                     const int64_t o = int64_t(m) * a.D + n0;
-                    const float* before = a.sums && !a.first ? a.sums + o : nullptr;
+                    if (a.sums && !a.first) add_row<false>(x, n, a.sums + o);
                     if (!a.last) {
-                        write_row(x, n, before, nullptr, a.sums + o, false);
+                        write_row<false>(x, n, a.sums + o);
+                    } else if (a.out_bf16) {
+                        uint16_t* out = static_cast<uint16_t*>(a.out) + o;
+                        if (a.accumulate) add_row<true>(x, n, out);
+                        write_row<true>(x, n, out);
                     } else {
-                        char* out = static_cast<char*>(a.out) + o * (a.out_bf16 ? 2 : 4);
-                        write_row(x, n, before, a.accumulate ? out : nullptr, out, a.out_bf16);
+                        float* out = static_cast<float*>(a.out) + o;
+                        if (a.accumulate) add_row<false>(x, n, out);
+                        write_row<false>(x, n, out);
                     }
                 }
             }
@@ -574,13 +588,15 @@ cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const 
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCtas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     note_launch();
     return cudaLaunchKernelEx(&cfg, loss_gemm_kernel<MODE, E, CAP, QUAD>, ta, tb, w);
 }
@@ -634,8 +650,7 @@ cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t
     if (!make_map(&ta, h, h_rows, a.D, a.D, 128) || !make_map(&tb, W, a.V, a.D, a.D, 128)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.V, kTile))};
     const int64_t tiles = up(a.rows, kTile) * w.n_nt;
-    bool quad = a.rows > kTile;
-    if (getenv("LG_LO")) quad = quad && atoi(getenv("LG_LO"));
+    const bool quad = a.rows > kTile;
     if (a.lm.cap > 0.f)
         return a.e ? launch<LOGITS, true, true>(ta, tb, w, tiles, quad, num_sms, stream)
                    : launch<LOGITS, false, true>(ta, tb, w, tiles, quad, num_sms, stream);
@@ -649,7 +664,6 @@ cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
     bool quad = w.n_nt > 1;
-    if (getenv("LG_DH")) quad = quad && atoi(getenv("LG_DH"));
     const int slots = quad ? quad_slots<DH, false, false>() : 0;
     quad = slots > 0;
     *grid = {w.n_nt, quad ? slots : num_sms / 2, quad};
@@ -663,9 +677,7 @@ cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
-    bool quad = w.n_nt > 1;
-    if (getenv("LG_DW")) quad = quad && atoi(getenv("LG_DW"));
-    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, quad, num_sms, stream);
+    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, w.n_nt > 1, num_sms, stream);
 }
 
 }  // namespace df2

@@ -51,6 +51,7 @@ live_rows_kernel(const LossRowsArgs a, const int each) {
     __shared__ int shared[kThreads / 32];
     __shared__ int place[kThreads];  // of the block's rows: its place among the live, -1: none
     __shared__ int so_far;
+    asm volatile("griddepcontrol.launch_dependents;");
     const int64_t first = int64_t(blockIdx.x) * each, last = dmin<int64_t>(first + each, a.P);
     auto alive = [&](int64_t p) { const int t = a.targets[p]; return t >= 0 && t < a.V; };
     int before = 0;
@@ -103,6 +104,8 @@ live_rows_kernel(const LossRowsArgs a, const int each) {
 template <bool G>
 __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a) {
     __shared__ float shared[kThreads / 32];
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t left = int64_t(*a.count) - a.row0;
     const int64_t live = left < 0 ? 0 : left > a.rows ? a.rows : left;
     const int64_t row = blockIdx.x;
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
             const int64_t at = c + k * kThreads * 8;
             if (at < c1) {
                 in[k] = __ldcs(reinterpret_cast<const uint4*>(e + at));
-                m[k] = __ldg(&stats[at / 128].x);
+                m[k] = __ldg(&stats[at / kLossStats].x);
             }
         }
 #pragma unroll
@@ -173,6 +176,8 @@ __global__ void __launch_bounds__(kThreads)
 sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* map, const float* part, int64_t V,
                  int64_t D, LossDhGrid grid, void* dh, bool bf16) {
     __shared__ int shared_splits;
+    asm volatile("griddepcontrol.launch_dependents;");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t left = int64_t(*count) - row0;
     const int64_t live = left < 0 ? 0 : left > rows ? rows : left;
     const int64_t row = blockIdx.x;
@@ -206,6 +211,24 @@ sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* ma
     }
 }
 
+// A launch whose start may overlap the end of the kernel before it in the stream: every thread
+// of these kernels waits for that one to be done before it reads or writes anything, so each is
+// also done with what came before.
+template <class... Params, class... Given>
+cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, cudaStream_t stream, Given... given) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    note_launch();
+    return cudaLaunchKernelEx(&cfg, kernel, Params(given)...);
+}
+
 }  // namespace
 
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream) {
@@ -220,25 +243,21 @@ cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream) {
 
 cudaError_t loss_row_launch(const LossRowArgs& a, int64_t e_rows, int num_sms, cudaStream_t stream) {
     if (!a.e) {
-        row_loss_kernel<false><<<unsigned(a.rows), kThreads, 0, stream>>>(a);
+        return launch_after(row_loss_kernel<false>, dim3(unsigned(a.rows)), stream, a);
     } else {
         // columns shared out where the rows alone leave SMs idle
         const int64_t rows = (a.rows + 63) / 64 * 64 < e_rows ? (a.rows + 63) / 64 * 64 : e_rows;
         int64_t shares = (8 * num_sms + a.rows - 1) / a.rows;
         const int64_t most = (a.V + 2047) / 2048;
         shares = shares > most ? most : shares;
-        row_loss_kernel<true><<<dim3(unsigned(rows), unsigned(shares)), kThreads, 0, stream>>>(a);
+        return launch_after(row_loss_kernel<true>, dim3(unsigned(rows), unsigned(shares)), stream, a);
     }
-    note_launch();
-    return cudaGetLastError();
 }
 
 cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, const LossDhGrid& grid, cudaStream_t stream) {
     const int64_t across = (a.D + 4 * kThreads - 1) / (4 * kThreads);
-    sum_parts_kernel<<<dim3(unsigned(a.rows), unsigned(across < 64 ? across : 64)), kThreads, 0, stream>>>(
-        a.count, a.row0, a.rows, a.map, a.part, a.V, a.D, grid, a.out, a.out_bf16);
-    note_launch();
-    return cudaGetLastError();
+    return launch_after(sum_parts_kernel, dim3(unsigned(a.rows), unsigned(across < 64 ? across : 64)), stream, a.count,
+                        a.row0, a.rows, a.map, static_cast<const float*>(a.part), a.V, a.D, grid, a.out, a.out_bf16);
 }
 
 }  // namespace df2

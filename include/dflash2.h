@@ -487,7 +487,7 @@ int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int6
  *   h [P, D] bf16; W_lm [V, D] bf16; targets [P] int32
  *   loss [P] fp32 out; lse [P] fp32 out, nullable
  *   workspace >= dflash2_unary_ce_workspace_size(P, D, V): a copy of h and at most 1 GiB of
- *             statistics of 128 columns each (more rows go in pieces), or 256 rows' where those
+ *             statistics of 64 columns each (more rows go in pieces), or 256 rows' where those
  *             are more
  * Rules: P >= 0, V >= 1, D >= 1, D % 8 == 0; output_multiplier and final_logit_softcapping as
  * dflash2_unary_topk; P < 2^31, V <= 2^24, D <= 2^20 (else DF2_ERR_UNSUPPORTED); outputs must
@@ -507,7 +507,7 @@ int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_
  * loss is not weighted; the gradients are those of sum_p w_p * loss_p.  A row without a target
  * contributes nothing: dh zero, its h and weight not used.
  * The factors g are rounded to bf16 for the products (2^-8 of each), whatever the gradients'
- * type, from exp(U' - M) held in fp16, M the largest of 128 columns (2^-11 of each, and 2^-40
+ * type, from exp(U' - M) held in fp16, M the largest of 64 columns (2^-11 of each, and 2^-40
  * of the largest).  Sums are fp32 in an
  * order the shapes and the rows with a target fix, so equal inputs give equal bits; dh and dW
  * are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it

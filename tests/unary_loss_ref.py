@@ -6,9 +6,9 @@ bit of a partial sum (2^-23 of it, and it is at most S = sum |h W|), added up in
 du = (D / 16 + 4) 2^-23 S.  The map multiplies by m (slope at most m) and rounds a few times:
 dx = m du + 2^-21 |x|.  exp turns dx, and the 2^-22 of its argument's product, into relative
 errors; a log-sum-exp is off by no more than its worst term, plus the rounding of sums of V
-terms in a tree of 128 columns a thread and of results of size |lse| and |x_t|.
+terms in a tree of 64 columns a thread and of results of size |lse| and |x_t|.
 A factor g is exp(x - lse) to those relative errors, rounded to fp16 (2^-11 of it, and in units of
-2^-39 of the largest of its 128 columns, which is at most the row's) and then to bf16 (2^-8);
+2^-39 of the largest of its 64 columns, which is at most the row's) and then to bf16 (2^-8);
 products of them are summed in n / 16 steps like the logits.
 """
 import torch
