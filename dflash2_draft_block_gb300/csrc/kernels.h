@@ -196,7 +196,7 @@ struct LossGemmArgs {
 constexpr int kLossSplits = 64;
 constexpr int64_t kLossPartial = int64_t(1) << 27;  // fp32 sums held at most
 __host__ __device__ inline int loss_split_limit(int64_t steps) {
-    const int64_t s = (steps + 15) / 16;
+    const int64_t s = (steps + 3) / 4;
     return int(s < kLossSplits ? s : kLossSplits);
 }
 // By a whole warp.

@@ -15,13 +15,16 @@
 // products came out 4e-6 of itself too small, which a loss would show.  The MMAs
 // therefore sum kSegment K elements at a time into one of two TMEM accumulators while the
 // epilogue warps add the other to running sums in fp32 registers (64 columns a thread, sixteen
-// warps), rounded to nearest.
+// warps), rounded to nearest.  dW's sums, of the rows of a piece and factors of 8 bits, stay one.
 //
 // Roles (640 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-19
 // are the epilogue (TMEM lane = row; four warps a quarter, 64 columns each).  Tiles are
 // dealt round-robin to the pairs.  Rows without a target were left out beforehand, so the
 // number of rows is read from the device.  All waits are bounded.
 #include <cudaTypedefs.h>
+
+#include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -192,34 +195,50 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
         make_float2(none ? top : CAP ? base : __fmul_rn(top, mul), (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
-// x += the columns [0, n) (n a multiple of 8) at p, 16 at a time: their loads are waited for once.
+// x += the columns [0, n) (n a multiple of 8) at p: their loads are waited for once.
 template <bool B16>
-__device__ __forceinline__ void add_row(float (&x)[kCols], int n, const void* p) {
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
+__device__ __forceinline__ void add_row(float (&x)[32], int n, const void* p) {
+    constexpr int kLoads = B16 ? 4 : 8, kEach = 32 / kLoads;
+    uint4 f[kLoads];
 #pragma unroll
-        for (int s = 0; s < 32; s += 16) {
-            constexpr int kLoads = B16 ? 2 : 4, kEach = 16 / kLoads;
-            const char* at = static_cast<const char*>(p) + (c + s) * (B16 ? 2 : 4);
-            uint4 f[kLoads];
+    for (int j = 0; j < kLoads; ++j)
+        f[j] = kEach * j < n ? static_cast<const uint4*>(p)[j] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                f[j] = c + s + kEach * j < n ? reinterpret_cast<const uint4*>(at)[j] : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < kLoads; ++j) {
+        const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (B16) {
-                        x[s + 8 * j + 2 * k] += bf16_lo(w[k]);
-                        x[s + 8 * j + 2 * k + 1] += bf16_hi(w[k]);
-                    } else {
-                        x[s + 4 * j + k] += __uint_as_float(w[k]);
-                    }
-                }
+        for (int k = 0; k < 4; ++k) {
+            if (B16) {
+                x[8 * j + 2 * k] += bf16_lo(w[k]);
+                x[8 * j + 2 * k + 1] += bf16_hi(w[k]);
+            } else {
+                x[4 * j + k] += __uint_as_float(w[k]);
             }
         }
-        turn(x);
+    }
+}
+
+// The first 32 of x, of which n (a multiple of 8) exist, to `to`.
+template <bool B16, int N>
+__device__ __forceinline__ void write32(const float (&x)[N], int n, void* to, bool wide) {
+    char* p = static_cast<char*>(to);
+    if (B16) {
+#pragma unroll
+        for (int s = 0; s < 32; s += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[s + 2 * j], x[s + 2 * j + 1]);
+            if (s + 16 <= n) store8(p + 2 * s, w, wide);
+            else if (s < n) *reinterpret_cast<uint4*>(p + 2 * s) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 32; s += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[s + j]);
+            if (s < n) store8(p + 4 * s, w, wide);
+        }
     }
 }
 
@@ -229,25 +248,7 @@ __device__ __forceinline__ void write_row(float (&x)[kCols], int n, void* out) {
     const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
 #pragma unroll 1
     for (int c = 0; c < kCols; c += 32) {
-        char* to = static_cast<char*>(out) + c * (B16 ? 2 : 4);
-        if (B16) {
-#pragma unroll
-            for (int s = 0; s < 32; s += 16) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = pack_bf16(x[s + 2 * j], x[s + 2 * j + 1]);
-                if (c + s + 16 <= n) store8(to + 2 * s, w, wide);
-                else if (c + s < n) *reinterpret_cast<uint4*>(to + 2 * s) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 32; s += 8) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[s + j]);
-                if (c + s < n) store8(to + 4 * s, w, wide);
-            }
-        }
+        write32<B16>(x, n - c, static_cast<char*>(out) + c * (B16 ? 2 : 4), wide);
         turn(x);
     }
 }
@@ -358,6 +359,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         return t;
     };
 
+    const int segment = MODE == DW ? max(k_total, 1) : kSegment;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegisters));
         if (warp == 0 && lane == 0) {
@@ -429,14 +431,14 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             bool ok = true;
             for (int i = unit; i < total && ok; i += units) {
                 const Tile t = tile(i);
-                for (int k = t.k0; k < t.k1 && ok; k += kSegment) {
+                for (int k = t.k0; k < t.k1 && ok; k += segment) {
                     if (!tc::mbar_wait_cluster(&tempty[buf], tphase ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
                     const uint32_t d = tmem_base + uint32_t(buf * kTile);
-                    const int end = min(k + kSegment, t.k1);
+                    const int end = min(k + segment, t.k1);
                     for (int kk = k; kk < end; ++kk) {
                         if (!tc::mbar_wait(&full[stage], phase, abort_flag)) {
                             ok = false;
@@ -484,37 +486,80 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(p + o));
                 }
             }
-            float x[kCols];
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) x[j] = 0.f;
-            for (int k = t.k0; k < t.k1; k += kSegment) {
-                ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
-                if (!ok) break;
-                tc::fence_after_sync();
+            if constexpr (MODE == DW) {
+                // straight from TMEM, 32 columns at a time: a sum of rows is one partial sum
+                const bool any = t.k1 > t.k0;
+                if (any) {
+                    ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                }
+                const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
                 const uint32_t taddr =
                     tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + part * kCols);
-#pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
+                const int64_t o = int64_t(m) * a.D + n0;
+#pragma unroll 1
+                for (int c = 0; c < n; c += 32) {
                     float v[32];
-                    tmem_ld32(taddr + c, v);
+                    if (any) {
+                        tmem_ld32(taddr + c, v);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) x[c + j] += v[j];
+                        for (int j = 0; j < 32; ++j) v[j] = 0.f;
+                    }
+                    if (m < a.V) {
+                        if (a.sums && !a.first) add_row<false>(v, n - c, a.sums + o + c);
+                        void* to = a.sums + o + c;
+                        if (a.last && a.out_bf16) to = static_cast<uint16_t*>(a.out) + o + c;
+                        else if (a.last) to = static_cast<float*>(a.out) + o + c;
+                        const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
+                        if (a.last && a.out_bf16) {
+                            if (a.accumulate) add_row<true>(v, n - c, to);
+                            write32<true>(v, n - c, to, wide);
+                        } else {
+                            if (a.last && a.accumulate) add_row<false>(v, n - c, to);
+                            write32<false>(v, n - c, to, wide);
+                        }
+                    }
+                    __syncwarp();  // whole again for the next load from TMEM
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
-                buf ^= 1;
-                if (buf == 0) tphase ^= 1;
-            }
-            if (!ok) break;
-            if (MODE == LOGITS) {
-                if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, part);
+                if (any) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1;
+                }
             } else {
-                const int n0 = t.nt * kTile + part * kCols;
-                const int n = min(kCols, int(a.D) - n0);
-                if (n <= 0) continue;
-                if (MODE == DH) {
-                    if (m < live) {
+                float x[kCols];
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) x[j] = 0.f;
+                for (int k = t.k0; k < t.k1; k += segment) {
+                    ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    const uint32_t taddr =
+                        tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + part * kCols);
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 32) {
+                        float v[32];
+                        tmem_ld32(taddr + c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) x[c + j] += v[j];
+                    }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1;
+                }
+                if (!ok) break;
+                if (MODE == LOGITS) {
+                    if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, part);
+                    __syncwarp();
+                } else {
+                    const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
+                    if (m < live && n > 0) {
                         if (splits > 1) {
                             write_row<false>(x, n, a.part + (int64_t(t.split) * live + m) * a.D + n0);
                         } else {
@@ -523,20 +568,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                             else write_row<false>(x, n, static_cast<float*>(a.out) + o);
                         }
                     }
-                } else if (m < a.V) {
-                    const int64_t o = int64_t(m) * a.D + n0;
-                    if (a.sums && !a.first) add_row<false>(x, n, a.sums + o);
-                    if (!a.last) {
-                        write_row<false>(x, n, a.sums + o);
-                    } else if (a.out_bf16) {
-                        uint16_t* out = static_cast<uint16_t*>(a.out) + o;
-                        if (a.accumulate) add_row<true>(x, n, out);
-                        write_row<true>(x, n, out);
-                    } else {
-                        float* out = static_cast<float*>(a.out) + o;
-                        if (a.accumulate) add_row<false>(x, n, out);
-                        write_row<false>(x, n, out);
-                    }
+                    __syncwarp();
                 }
             }
         }
@@ -577,14 +609,28 @@ bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int6
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The kernels' shared memory is the same for every call: allowed once on each device.
 template <int MODE, bool E, bool CAP, bool QUAD>
-cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, int64_t clusters,
+cudaError_t smem_once() {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = allow_smem<loss_gemm_kernel<MODE, E, CAP, QUAD>>(kSmem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+}
+
+template <int MODE, bool E, bool CAP, bool QUAD>
+cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t clusters,
                             cudaStream_t stream) {
-    const cudaError_t e = allow_smem<loss_gemm_kernel<MODE, E, CAP, QUAD>>(kSmem);
+    const cudaError_t e = smem_once<MODE, E, CAP, QUAD>();
     if (e != cudaSuccess) return e;
     constexpr unsigned kCtas = QUAD ? 4 : 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas * unsigned(clusters < tiles ? clusters : tiles));
+    cfg.gridDim = dim3(kCtas * unsigned(clusters));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
@@ -612,7 +658,7 @@ int quad_slots() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
     std::lock_guard<std::mutex> lock(mu);
     if (known[dev] == 0) {
-        if (allow_smem<loss_gemm_kernel<MODE, E, CAP, true>>(kSmem) != cudaSuccess) return 0;
+        if (smem_once<MODE, E, CAP, true>() != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(4);
         cfg.blockDim = dim3(kThreads);
@@ -630,14 +676,14 @@ int quad_slots() {
     return known[dev] - 1;
 }
 
+// `across` tiles by `shared` ones that neighbours share an operand along.
 template <int MODE, bool E = false, bool CAP = false>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t tiles, bool quad, int num_sms,
-                   cudaStream_t stream) {
-    if (quad) {
-        const int slots = quad_slots<MODE, E, CAP>();
-        if (slots > 0) return launch_clusters<MODE, E, CAP, true>(ta, tb, w, slots, slots, stream);
-    }
-    return launch_clusters<MODE, E, CAP, false>(ta, tb, w, tiles, num_sms / 2, stream);
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t across, int64_t shared,
+                   int num_sms, cudaStream_t stream) {
+    const int slots = shared > 1 ? quad_slots<MODE, E, CAP>() : 0;
+    const int64_t tiles = loss_cluster_tiles(int(across), int(shared), slots > 0);
+    if (slots > 0) return launch_clusters<MODE, E, CAP, true>(ta, tb, w, tiles < slots ? tiles : slots, stream);
+    return launch_clusters<MODE, E, CAP, false>(ta, tb, w, tiles < num_sms / 2 ? tiles : num_sms / 2, stream);
 }
 
 int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
@@ -649,13 +695,12 @@ cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, h, h_rows, a.D, a.D, 128) || !make_map(&tb, W, a.V, a.D, a.D, 128)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.V, kTile))};
-    const int64_t tiles = up(a.rows, kTile) * w.n_nt;
-    const bool quad = a.rows > kTile;
+    const int64_t rows = up(a.rows, kTile);
     if (a.lm.cap > 0.f)
-        return a.e ? launch<LOGITS, true, true>(ta, tb, w, tiles, quad, num_sms, stream)
-                   : launch<LOGITS, false, true>(ta, tb, w, tiles, quad, num_sms, stream);
-    return a.e ? launch<LOGITS, true, false>(ta, tb, w, tiles, quad, num_sms, stream)
-               : launch<LOGITS, false, false>(ta, tb, w, tiles, quad, num_sms, stream);
+        return a.e ? launch<LOGITS, true, true>(ta, tb, w, w.n_nt, rows, num_sms, stream)
+                   : launch<LOGITS, false, true>(ta, tb, w, w.n_nt, rows, num_sms, stream);
+    return a.e ? launch<LOGITS, true, false>(ta, tb, w, w.n_nt, rows, num_sms, stream)
+               : launch<LOGITS, false, false>(ta, tb, w, w.n_nt, rows, num_sms, stream);
 }
 
 cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int num_sms, LossDhGrid* grid,
@@ -664,12 +709,14 @@ cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
     bool quad = w.n_nt > 1;
-    const int slots = quad ? quad_slots<DH, false, false>() : 0;
+    int slots = quad ? quad_slots<DH, false, false>() : 0;
     quad = slots > 0;
-    *grid = {w.n_nt, quad ? slots : num_sms / 2, quad};
-    // every cluster that fits: the splits share the rows that turn out to be live among them
-    return quad ? launch_clusters<DH, false, false, true>(ta, tb, w, slots, slots, stream)
-                : launch_clusters<DH, false, false, false>(ta, tb, w, num_sms / 2, num_sms / 2, stream);
+    if (!quad) slots = num_sms / 2;
+    // a cluster for each part there can be: how many there are follows from the live rows
+    const int64_t most = int64_t(loss_cluster_tiles(int(up(a.rows, kTile)), w.n_nt, quad)) * loss_split_limit(up(a.V, kStep));
+    *grid = {w.n_nt, int(most < slots ? most : slots), quad};
+    return quad ? launch_clusters<DH, false, false, true>(ta, tb, w, grid->units, stream)
+                : launch_clusters<DH, false, false, false>(ta, tb, w, grid->units, stream);
 }
 
 cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
@@ -677,7 +724,7 @@ cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
-    return launch<DW>(ta, tb, w, up(a.V, kTile) * w.n_nt, w.n_nt > 1, num_sms, stream);
+    return launch<DW>(ta, tb, w, up(a.V, kTile), w.n_nt, num_sms, stream);
 }
 
 }  // namespace df2
