@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "loss_tiles.h"
+
 namespace df2 {
 
 // The unary logits' output multiplier and final softcap: u -> cap * tanh(mul * u / cap),
@@ -164,7 +166,6 @@ struct LossRowsArgs {
 };
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream);
 
-constexpr int kLossStats = 64;          // columns that share a maximum
 constexpr float kExpScale = 32768.f;  // exp(x - M) is held in fp16 in units of 2^-15
 struct LossGemmArgs {
     const int32_t* count;
@@ -189,24 +190,11 @@ struct LossGemmArgs {
     bool first, last, accumulate;
 };
 
-// How many ways dh's product is split along V, for `tiles` tiles of `steps` steps (of 64) on
-// `units` clusters: the busiest cluster's steps at 0.3 us, and the partial sums' way out and
-// back at 4 TB/s, in ns.  The live rows decide, so it is worked out on the device, by each
-// kernel that needs it; in whole numbers, so that all find the same.
-constexpr int kLossSplits = 64;
-constexpr int64_t kLossPartial = int64_t(1) << 27;  // fp32 sums held at most
-__host__ __device__ inline int loss_split_limit(int64_t steps) {
-    const int64_t s = (steps + 3) / 4;
-    return int(s < kLossSplits ? s : kLossSplits);
-}
-// By a whole warp.
+// The split of dh's product (loss_tiles.h), by a whole warp.
 __device__ __forceinline__ int loss_splits(int64_t tiles, int64_t steps, int64_t units, int64_t rows, int64_t D, int lane) {
-    const int limit = loss_split_limit(steps);
     int64_t best = INT64_MAX;
-    for (int s = lane + 1; s <= limit && (s == 1 || s * rows * D <= kLossPartial); s += 32) {
-        int64_t ns = (tiles * s + units - 1) / units * ((steps + s - 1) / s) * 300;
-        if (s > 1) ns += 3000 + s * rows * D * 2 / 1000;
-        const int64_t key = ns * 128 + s;  // equal times: the fewer
+    for (int s = lane + 1; s <= loss_split_limit(steps); s += 32) {
+        const int64_t key = loss_split_key(s, tiles, steps, units, rows, D);
         best = key < best ? key : best;
     }
     for (int o = 16; o; o >>= 1) {
@@ -214,11 +202,6 @@ __device__ __forceinline__ int loss_splits(int64_t tiles, int64_t steps, int64_t
         best = other < best ? other : best;
     }
     return int(best & 127);
-}
-// Tiles of clusters: `across` by `shared`; quads take the shared index by twos, and where it is
-// odd the last of it with the other index by twos.
-__host__ __device__ inline int loss_cluster_tiles(int across, int shared, bool quad) {
-    return quad ? across * (shared / 2) + (shared & 1) * ((across + 1) / 2) : across * shared;
 }
 struct LossDhGrid {
     int n_nt, units;          // N tiles, clusters

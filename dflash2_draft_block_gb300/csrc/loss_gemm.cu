@@ -44,7 +44,6 @@ constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
 constexpr int kStages = 7;
 constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
-constexpr int kGroup = 16;                     // M units that share a pass over W (8: 3% slower; 32: 2%)
 constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
 constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
 
@@ -319,45 +318,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const int splits = MODE == DH ? loss_splits(tiles, k_total, units, live, a.D, lane) : 1;
     const int total = tiles * splits;
 
-    // tile i: its M unit, N tile and stages [k0, k1).  alone: the pairs of a cluster share
-    // nothing (the odd M unit or N tile at the end, whose other index they take by twos).
-    struct Tile {
-        int mu, nt, split, k0, k1;
-        bool alone;
-    };
-    auto tile = [&](int i) {
-        Tile t;
-        t.split = i / tiles;
-        const int j = i - t.split * tiles;
-        t.alone = false;
-        if (MODE == LOGITS) {  // M fastest in groups: W streams past, a group's rows of h stay in L2
-            constexpr int kRun = kGroup / kPairs;
-            const int n_m = n_mu / kPairs, odd = j - n_m * n_nt;
-            if (odd < 0) {
-                const int first = j / (kRun * n_nt) * kRun;
-                const int wide = min(kRun, n_m - first), rest = j - first * n_nt;
-                t.mu = (first + rest % wide) * kPairs + which;
-                t.nt = rest / wide;
-            } else {
-                t.mu = n_mu - 1;
-                t.nt = odd * 2 + which;
-                t.alone = true;
-            }
-        } else {               // N fastest: the clusters of a moment share g's rows
-            const int n_n = n_nt / kPairs, odd = j - n_mu * n_n;
-            if (odd < 0) {
-                t.nt = j % n_n * kPairs + which;
-                t.mu = j / n_n;
-            } else {
-                t.nt = n_nt - 1;
-                t.mu = odd * 2 + which;
-                t.alone = true;
-            }
-        }
-        t.k0 = int(int64_t(k_total) * t.split / splits);
-        t.k1 = int(int64_t(k_total) * (t.split + 1) / splits);
-        return t;
-    };
+    auto tile = [&](int i) { return loss_tile<MODE == LOGITS, QUAD>(i, n_mu, n_nt, splits, k_total, which); };
 
     const int segment = MODE == DW ? max(k_total, 1) : kSegment;
     if (warp < 4) {
@@ -373,7 +334,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             for (int s = 0; s < kStages; ++s) armed[s] = -1;
             bool ok = true;
             for (int i = unit; i < total && ok; i += units) {
-                const Tile t = tile(i);
+                const LossTile t = tile(i);
                 for (int k = t.k0; k < t.k1; ++k) {
                     if (!tc::mbar_wait(&empty[stage], phase ^ 1, abort_flag)) {
                         ok = false;
@@ -430,7 +391,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             uint32_t phase = 0, tphase = 0;
             bool ok = true;
             for (int i = unit; i < total && ok; i += units) {
-                const Tile t = tile(i);
+                const LossTile t = tile(i);
                 for (int k = t.k0; k < t.k1 && ok; k += segment) {
                     if (!tc::mbar_wait_cluster(&tempty[buf], tphase ^ 1, abort_flag)) {
                         ok = false;
@@ -474,7 +435,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         uint32_t tphase = 0;
         bool ok = true;
         for (int i = unit; i < total && ok; i += units) {
-            const Tile t = tile(i);
+            const LossTile t = tile(i);
             const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
             if (MODE == DW && a.last && a.accumulate && m < a.V) {
                 // what dW holds is on its way while the product is summed
