@@ -1,6 +1,6 @@
 """Train a candidate selector on the GPU: every training operator in the order of a step.
 
-    python examples/train_selector.py [--steps 60] [--state-bits 8]
+    python examples/train_selector.py [--steps 60] [--state-bits 8] [--head-loss 0.1] [--dropout 0.1]
 
 The task is synthetic: a table says how well each class of token follows each predecessor,
 and the right token of a position is the candidate that follows best.  The unary logits
@@ -12,6 +12,13 @@ do not know the table; the codebooks can learn it.  A step is
     dW_H    = dG^T h,  dh = dG W_H                      (plain matrix products)
     dE      = embedding_grad(dh, context)
     AdamW over E, W_H, A and Bc: bf16 weights with fp32 masters, states in 8 or 32 bits
+
+With --head-loss the cross-entropy of the unary logits over the whole vocabulary joins in, by
+its share, through a frozen head, and with --dropout h is dropped at that rate:
+
+    h       = dropout(h, rate, seed, step)
+    loss, lse, dh', _ = unary_loss_grad(h, W_lm, targets)         dh += share * dh'
+    dh      = dropout_grad(dh, rate, seed, step)
 """
 from __future__ import annotations
 
@@ -26,7 +33,8 @@ import torch  # noqa: E402
 import dflash2_draft_block_gb300 as df2  # noqa: E402
 
 
-def train(steps=60, positions=2048, vocab=4096, hidden=256, rank=64, top_k=16, state_bits=8, seed=0):
+def train(steps=60, positions=2048, vocab=4096, hidden=256, rank=64, top_k=16, state_bits=8, seed=0, head_loss=0.0,
+          dropout=0.0):
     """The mean loss of every step (rows whose right token is a candidate)."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
 
@@ -43,11 +51,13 @@ def train(steps=60, positions=2048, vocab=4096, hidden=256, rank=64, top_k=16, s
                     master_weights=True)
     scale = hidden ** -0.5
     losses = []
-    for _ in range(steps):
+    for step in range(steps):
         context = torch.randint(0, vocab, (positions,), generator=gen, device="cuda", dtype=torch.int32)
         context[:: 16] = -1                                      # padding
         pred = torch.randint(0, classes, (positions,), generator=gen, device="cuda", dtype=torch.int32)
         h = df2.embedding(E, context, scale=scale)
+        if dropout:
+            h = df2.dropout(h, dropout, seed, step)
         ids, vals, G = df2.unary_topk(h, W_lm, top_k, W_H)
         column = follows[pred.long()].gather(1, ids.long() % classes).argmax(dim=1)
         targets = ids.gather(1, column[:, None])[:, 0]
@@ -55,7 +65,12 @@ def train(steps=60, positions=2048, vocab=4096, hidden=256, rank=64, top_k=16, s
         loss, label, dscores, dG, _, _ = df2.selector_loss_grad(pred, targets, ids, vals, G, A, Bc,
                                                                 dA=grads[2], dBc=grads[3])
         grads[1].copy_(dG.t() @ h.float())
-        df2.embedding_grad(dG @ W_H.float(), context, vocab, scale=scale, out=grads[0])
+        dh = dG @ W_H.float()
+        if head_loss:
+            dh += head_loss * df2.unary_loss_grad(h, W_lm, targets, dtype=torch.float32)[2]
+        if dropout:
+            dh = df2.dropout_grad(dh, dropout, seed, step)
+        df2.embedding_grad(dh, context, vocab, scale=scale, out=grads[0])
         # gradients of the sum so far: the mean's by the optimiser (no counted row: no step)
         counted = (label >= 0).sum()
         opt.step(grad_scale=(1.0 / counted.float()).reshape(1))
@@ -67,8 +82,10 @@ def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--state-bits", type=int, default=8, choices=(8, 32))
+    ap.add_argument("--head-loss", type=float, default=0.0)
+    ap.add_argument("--dropout", type=float, default=0.0)
     a = ap.parse_args()
-    losses = train(a.steps, state_bits=a.state_bits)
+    losses = train(a.steps, state_bits=a.state_bits, head_loss=a.head_loss, dropout=a.dropout)
     for i in range(0, len(losses), max(1, len(losses) // 10)):
         print(f"step {i:4d}  loss {losses[i]:.4f}")
     print(f"step {len(losses) - 1:4d}  loss {losses[-1]:.4f}")
