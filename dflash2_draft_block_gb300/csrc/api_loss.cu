@@ -7,6 +7,9 @@
 
 namespace {
 
+// Positions a call: the blocks that put the rows with a target in order each count the ones
+// before them, which is P^2 / 256 or so of reading (2 ms at 2^20).
+constexpr int64_t kMaxRows = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kMaxHidden = int64_t(1) << 20;
 // what a piece of rows may take: exponentials in bf16 (the gradients), or statistics (the loss
@@ -25,7 +28,7 @@ int num_sms_current() {
 
 int check_shape(int64_t P, int64_t D, int64_t V) {
     if (P < 0 || D < 1 || V < 1) return DF2_ERR_INVALID_ARGUMENT;
-    if (D % 8 != 0 || P > INT32_MAX || D > kMaxHidden || V > kMaxVocab) return DF2_ERR_UNSUPPORTED;
+    if (D % 8 != 0 || P > kMaxRows || D > kMaxHidden || V > kMaxVocab) return DF2_ERR_UNSUPPORTED;
     return DF2_OK;
 }
 

@@ -133,7 +133,7 @@ def test_library_refusals():
                 dict(dh=base), dict(dh=2 * base), dict(dW=2 * base + 16), dict(dW=6 * base), dict(loss=5 * base + 4),
                 dict(lse=4 * base), dict(loss=3 * base), dict(loss=6 * base + 8)):
         assert call(**bad) == 1, bad
-    for bad in (dict(D=20), dict(P=1 << 31), dict(D=(1 << 20) + 8), dict(V=(1 << 24) + 1), dict(h=base + 8), dict(W=2 * base + 2),
+    for bad in (dict(D=20), dict(P=(1 << 20) + 1), dict(D=(1 << 20) + 8), dict(V=(1 << 24) + 1), dict(h=base + 8), dict(W=2 * base + 2),
                 dict(dh=6 * base + 8), dict(dW=7 * base + 4), dict(t=3 * base + 2), dict(loss=4 * base + 1),
                 dict(lse=5 * base + 2), dict(w=9 * base + 1)):
         assert call(**bad) == 2, bad
