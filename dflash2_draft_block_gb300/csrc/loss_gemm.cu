@@ -61,6 +61,14 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
     return d;
 }
 
+// This warp has read its part of an accumulator (its loads are complete): an arrive that orders
+// nothing else.  One with release would wait until the rows stored before are in memory.
+__device__ __forceinline__ void accumulator_read(uint64_t* bar, uint32_t lead) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     tc::mapa_shared(tc::smem_u32(bar), lead))
+                 : "memory");
+}
+
 // 32 lanes x 32 consecutive columns, ready on return.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float v[32]) {
     uint32_t r[32];
@@ -487,7 +495,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 if (any) {
                     tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
+                    if (lane == 0) accumulator_read(&tempty[buf], lead);
                     buf ^= 1;
                     if (buf == 0) tphase ^= 1;
                 }
@@ -510,7 +518,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     }
                     tc::fence_before_sync();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty[buf]), lead));
+                    if (lane == 0) accumulator_read(&tempty[buf], lead);
                     buf ^= 1;
                     if (buf == 0) tphase ^= 1;
                 }
