@@ -203,25 +203,17 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
 }
 
 // x += the columns [0, n) (n a multiple of 8) at p: their loads are waited for once.
-template <bool B16>
-__device__ __forceinline__ void add_row(float (&x)[32], int n, const void* p) {
-    constexpr int kLoads = B16 ? 4 : 8, kEach = 32 / kLoads;
-    uint4 f[kLoads];
+__device__ __forceinline__ void add_row(float (&x)[32], int n, const float* p) {
+    float4 f[8];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j)
-        f[j] = kEach * j < n ? static_cast<const uint4*>(p)[j] : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < 8; ++j)
+        f[j] = 4 * j < n ? reinterpret_cast<const float4*>(p)[j] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-        const uint32_t w[4] = {f[j].x, f[j].y, f[j].z, f[j].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (B16) {
-                x[8 * j + 2 * k] += bf16_lo(w[k]);
-                x[8 * j + 2 * k + 1] += bf16_hi(w[k]);
-            } else {
-                x[4 * j + k] += __uint_as_float(w[k]);
-            }
-        }
+    for (int j = 0; j < 8; ++j) {
+        x[4 * j] += f[j].x;
+        x[4 * j + 1] += f[j].y;
+        x[4 * j + 2] += f[j].z;
+        x[4 * j + 3] += f[j].w;
     }
 }
 
@@ -445,30 +437,33 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         for (int i = unit; i < total && ok; i += units) {
             const LossTile t = tile(i);
             const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
-            if (MODE == DW && a.last && a.accumulate && m < a.V) {
-                // what dW holds is on its way while the product is summed
-                const int n0 = t.nt * kTile + part * kCols;
-                if (n0 < a.D) {
-                    const int64_t size = a.out_bf16 ? 2 : 4;
-                    const char* p = static_cast<const char*>(a.out) + (int64_t(m) * a.D + n0) * size;
-                    for (int64_t o = 0; o < kCols * size && n0 + o / size < a.D; o += 128)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(p + o));
-                }
-            }
             if constexpr (MODE == DW) {
-                // straight from TMEM, 32 columns at a time: a sum of rows is one partial sum
+                // straight from TMEM, 32 columns at a time: a sum of rows is one partial sum.  What a
+                // bf16 dW holds is on its way while the product is summed; an fp32 one's, to L2.
                 const bool any = t.k1 > t.k0;
+                const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
+                const int64_t o = int64_t(m) * a.D + n0;
+                uint4 old[kCols / 8];
+                const bool plus16 = a.last && a.accumulate && a.out_bf16;
+#pragma unroll
+                for (int j = 0; j < kCols / 8; ++j)
+                    old[j] = plus16 && m < a.V && 8 * j < n
+                                 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.out) + o)[j]
+                                 : make_uint4(0u, 0u, 0u, 0u);
+                if (a.last && a.accumulate && !a.out_bf16 && m < a.V && n > 0) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<float*>(a.out) + o));
+                    if (n > 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<float*>(a.out) + o + 32));
+                }
                 if (any) {
                     ok = __all_sync(kFull, tc::mbar_wait(&tfull[buf], tphase, abort_flag));
                     if (!ok) break;
                     tc::fence_after_sync();
                 }
-                const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
                 const uint32_t taddr =
                     tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + part * kCols);
-                const int64_t o = int64_t(m) * a.D + n0;
-#pragma unroll 1
-                for (int c = 0; c < n; c += 32) {
+#pragma unroll
+                for (int c = 0; c < kCols; c += 32) {
+                    if (c >= n) break;
                     float v[32];
                     if (any) {
                         tmem_ld32(taddr + c, v);
@@ -477,16 +472,22 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                         for (int j = 0; j < 32; ++j) v[j] = 0.f;
                     }
                     if (m < a.V) {
-                        if (a.sums && !a.first) add_row<false>(v, n - c, a.sums + o + c);
+                        if (a.sums && !a.first) add_row(v, n - c, a.sums + o + c);
                         void* to = a.sums + o + c;
                         if (a.last && a.out_bf16) to = static_cast<uint16_t*>(a.out) + o + c;
                         else if (a.last) to = static_cast<float*>(a.out) + o + c;
                         const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
                         if (a.last && a.out_bf16) {
-                            if (a.accumulate) add_row<true>(v, n - c, to);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float f[8];
+                                unpack8(old[c / 8 + j], f);
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) v[8 * j + k] += f[k];
+                            }
                             write32<true>(v, n - c, to, wide);
                         } else {
-                            if (a.last && a.accumulate) add_row<false>(v, n - c, to);
+                            if (a.last && a.accumulate) add_row(v, n - c, static_cast<const float*>(to));
                             write32<false>(v, n - c, to, wide);
                         }
                     }
