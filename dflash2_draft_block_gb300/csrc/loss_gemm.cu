@@ -42,10 +42,13 @@ constexpr int kCols = kLossStats;              // columns of an epilogue thread
 constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
-constexpr int kStages = 7;
 constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
-constexpr uint32_t kBarriers = (2 * kStages + 5) * 8 + 16;
-constexpr uint32_t kSmem = kStages * 2 * kOperand + kBarriers + 1024;
+constexpr int kStagedSteps = 32;               // dW's sums of up to 64 times this many rows go out staged
+constexpr uint32_t kStaging = 4096;            // bytes of an epilogue warp: 128 of each of its 32 rows
+__host__ __device__ constexpr int stages(bool staged) { return staged ? 5 : 7; }
+__host__ __device__ constexpr uint32_t smem_bytes(bool staged) {
+    return stages(staged) * 2 * kOperand + (staged ? 16 * kStaging : 0) + (2 * stages(staged) + 5 + 16) * 8 + 16 + 1024;
+}
 
 enum { LOGITS, DH, DW };
 
@@ -252,24 +255,123 @@ __device__ __forceinline__ void write_row(float (&x)[kCols], int n, void* out) {
     }
 }
 
+// A warp's 32 rows and 64 columns of dW from (m0, n0), through its staging: 128 bytes a row at a
+// time, as TMA swizzles them.  there: the tile is in dW; any: there is a sum in TMEM, whose
+// barrier is waited for.  False where a wait gave up.
+template <bool B16>
+__device__ __forceinline__ bool staged_tile(const CUtensorMap& map, bool plus, bool there, bool any, int n0, int m0, int D,
+                                            uint32_t taddr, uint8_t* staging, uint64_t* loaded, uint32_t* loaded_phase,
+                                            uint64_t* tfull, uint32_t tphase, int lane, volatile int* abort_flag) {
+    constexpr int kWide = B16 ? 64 : 32;  // columns of 128 bytes
+    auto begin = [&](int c) {  // the staging is free again; what is added to comes in
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            if (plus) {
+                tc::mbar_arrive_expect_tx(loaded, kStaging);
+                tc::tma_load_2d(staging, &map, loaded, n0 + c, m0, tc::l2_policy_evict_first());
+            }
+        }
+        __syncwarp();
+    };
+    if (there) begin(0);
+    bool ok = true;
+    if (any) {
+        ok = __all_sync(kFull, tc::mbar_wait(tfull, tphase, abort_flag));
+        tc::fence_after_sync();
+    }
+    if (there && plus && !ok) {  // the copy in flight ends before the block does
+        volatile int never = 0;
+        tc::mbar_wait(loaded, *loaded_phase, &never);
+    }
+    if (!ok || !there) return ok;
+    uint4* own = reinterpret_cast<uint4*>(staging + lane * 128);
+#pragma unroll 1
+    for (int c = 0; c < kCols; c += kWide) {
+        if (n0 + c >= D) break;
+        if (c > 0) begin(c);
+        if (plus) {
+            ok = __all_sync(kFull, tc::mbar_wait(loaded, *loaded_phase, abort_flag));
+            if (!ok) {
+                volatile int never = 0;
+                tc::mbar_wait(loaded, *loaded_phase, &never);
+                return false;
+            }
+            *loaded_phase ^= 1;
+        }
+#pragma unroll
+        for (int s = 0; s < kWide; s += 32) {
+            float v[32];
+            if (any) {
+                tmem_ld32(taddr + c + s, v);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.f;
+            }
+            constexpr int kEach = B16 ? 8 : 4;  // columns of 16 bytes
+#pragma unroll
+            for (int j = 0; j < 32; j += kEach) {
+                uint4* at = own + (((s + j) / kEach) ^ (lane & 7));
+                if (plus) {
+                    const uint4 o = *at;
+                    if (B16) {
+                        float f[8];
+                        unpack8(o, f);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) v[j + (k % kEach)] += f[k];
+                    } else {
+                        v[j] += __uint_as_float(o.x);
+                        v[j + 1] += __uint_as_float(o.y);
+                        v[j + 2] += __uint_as_float(o.z);
+                        v[j + 3] += __uint_as_float(o.w);
+                    }
+                }
+                if constexpr (B16)
+                    *at = make_uint4(pack_bf16(v[j], v[j + 1]), pack_bf16(v[j + 2], v[j + 3]), pack_bf16(v[j + 4], v[j + 5]),
+                                     pack_bf16(v[j + 6], v[j + 7]));
+                else
+                    *at = make_uint4(__float_as_uint(v[j]), __float_as_uint(v[j + 1]), __float_as_uint(v[j + 2]),
+                                     __float_as_uint(v[j + 3]));
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             reinterpret_cast<uint64_t>(&map)),
+                         "r"(n0 + c), "r"(m0), "r"(tc::smem_u32(staging))
+                         : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+    return true;
+}
+
 // QUAD: a cluster of two pairs on neighbouring tiles that share an operand (LOGITS: two M units
 // and W's rows; the gradients: two N tiles and g's): the first pair's CTAs load it for the CTA
 // of the same rank in the other pair too, and a stage is free when both pairs' MMAs have read
 // it.  A tile past the end is computed on zeros and not written.
-template <int MODE, bool E, bool CAP, bool QUAD>
+// STAGED (dW, one piece): rows go out, and what they are added to comes in, by TMA through a
+// staging of each epilogue warp, for short products, whose time is the tile's way out: a row a
+// lane costs the memory pipeline a cycle for each 16 bytes.  64 rows x 151,936 x 4096 in bf16: 225
+// us (5.5 TB/s) instead of 290, added to old values 420 (5.9 TB/s) instead of 660; 1,024 rows 4%
+// of the whole call, 2,048 2%, and none added.  It takes two stages of the ring.
+template <int MODE, bool E, bool CAP, bool QUAD, bool STAGED>
 __global__ void __launch_bounds__(kThreads, 1)
 loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                 const __grid_constant__ Work w) {
+                 const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Work w) {
+    constexpr int kStages = stages(STAGED);
     constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
     const LossGemmArgs& a = w.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + size_t(kStages) * 2 * kOperand);
+    uint8_t* staging = smem + size_t(kStages) * 2 * kOperand;
+    uint64_t* full = reinterpret_cast<uint64_t*>(staging + (STAGED ? 16 * kStaging : 0));
     uint64_t* empty = full + kStages;
     uint64_t* tfull = empty + kStages;
     uint64_t* tempty = tfull + 2;
     uint64_t* mma_done = tempty + 2;
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(mma_done + 1);
+    uint64_t* loaded = mma_done + 1;  // of the epilogue warps
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(loaded + 16);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,6 +390,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             tc::mbar_init(&tempty[b], 32);  // the epilogue warps of both CTAs
         }
         tc::mbar_init(mma_done, 1);
+        for (int i = 0; i < 16; ++i) tc::mbar_init(&loaded[i], 1);
         *abort_flag = 0;
         tc::fence_mbar_init();
     }
@@ -298,6 +401,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     if (warp == 0 && lane == 0) {
         tc::prefetch_tmap(&tm_a);
         tc::prefetch_tmap(&tm_b);
+        if (STAGED) tc::prefetch_tmap(&tm_out);
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -432,12 +536,31 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegisters));
         const int quarter = warp & 3, part = (warp >> 2) - 1;
         int buf = 0;
-        uint32_t tphase = 0;
+        uint32_t tphase = 0, loaded_phase = 0;
         bool ok = true;
         for (int i = unit; i < total && ok; i += units) {
             const LossTile t = tile(i);
             const int m = t.mu * kTile + rank * 128 + quarter * 32 + lane;
-            if constexpr (MODE == DW) {
+            if constexpr (STAGED) {
+                const int m0 = m - lane, n0 = t.nt * kTile + part * kCols;
+                const bool there = m0 < a.V && n0 < a.D, any = t.k1 > t.k0;
+                const uint32_t taddr =
+                    tmem_base + (uint32_t(quarter * 32) << 16) + uint32_t(buf * kTile + part * kCols);
+                if (a.out_bf16)
+                    ok = staged_tile<true>(tm_out, a.accumulate, there, any, n0, m0, int(a.D), taddr, staging + (warp - 4) * kStaging,
+                                           &loaded[warp - 4], &loaded_phase, &tfull[buf], tphase, lane, abort_flag);
+                else
+                    ok = staged_tile<false>(tm_out, a.accumulate, there, any, n0, m0, int(a.D), taddr, staging + (warp - 4) * kStaging,
+                                            &loaded[warp - 4], &loaded_phase, &tfull[buf], tphase, lane, abort_flag);
+                if (!ok) break;
+                if (any) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) accumulator_read(&tempty[buf], lead);
+                    buf ^= 1;
+                    if (buf == 0) tphase ^= 1;
+                }
+            } else if constexpr (MODE == DW) {
                 // straight from TMEM, 32 columns at a time: a sum of rows is one partial sum.  What a
                 // bf16 dW holds is on its way while the product is summed; an fp32 one's, to L2.
                 const bool any = t.k1 > t.k0;
@@ -542,6 +665,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
             }
         }
+        if (STAGED && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
 
     tc::fence_before_sync();
@@ -568,19 +692,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// Boxes of 64 elements of a row by box_rows rows.
-bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+// Boxes of 128 bytes of a row by box_rows rows.
+bool make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f32 = false) {
     auto fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld) * 2};
-    const cuuint32_t box[2] = {64, cuuint32_t(box_rows)}, estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(ld) * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {f32 ? 32u : 64u, cuuint32_t(box_rows)}, estr[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The kernels' shared memory is the same for every call: allowed once on each device.
-template <int MODE, bool E, bool CAP, bool QUAD>
+template <int MODE, bool E, bool CAP, bool QUAD, bool STAGED>
 cudaError_t smem_once() {
     static std::atomic<uint64_t> done{0};
     int dev = 0;
@@ -588,21 +712,21 @@ cudaError_t smem_once() {
     if (e != cudaSuccess) return e;
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
-    e = allow_smem<loss_gemm_kernel<MODE, E, CAP, QUAD>>(kSmem);
+    e = allow_smem<loss_gemm_kernel<MODE, E, CAP, QUAD, STAGED>>(smem_bytes(STAGED));
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
     return e;
 }
 
-template <int MODE, bool E, bool CAP, bool QUAD>
-cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t clusters,
+template <int MODE, bool E, bool CAP, bool QUAD, bool STAGED>
+cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Work& w, int64_t clusters,
                             cudaStream_t stream) {
-    const cudaError_t e = smem_once<MODE, E, CAP, QUAD>();
+    const cudaError_t e = smem_once<MODE, E, CAP, QUAD, STAGED>();
     if (e != cudaSuccess) return e;
     constexpr unsigned kCtas = QUAD ? 4 : 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kCtas * unsigned(clusters));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
+    cfg.dynamicSmemBytes = smem_bytes(STAGED);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -614,12 +738,12 @@ cudaError_t launch_clusters(const CUtensorMap& ta, const CUtensorMap& tb, const 
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     note_launch();
-    return cudaLaunchKernelEx(&cfg, loss_gemm_kernel<MODE, E, CAP, QUAD>, ta, tb, w);
+    return cudaLaunchKernelEx(&cfg, loss_gemm_kernel<MODE, E, CAP, QUAD, STAGED>, ta, tb, to, w);
 }
 
 // Clusters of two pairs (four SMs of one GPC) that run at once on the current device, asked
 // once; 0 where the question fails.
-template <int MODE, bool E, bool CAP>
+template <int MODE, bool E, bool CAP, bool STAGED>
 int quad_slots() {
     constexpr int kDevices = 64;
     static std::mutex mu;
@@ -628,11 +752,11 @@ int quad_slots() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
     std::lock_guard<std::mutex> lock(mu);
     if (known[dev] == 0) {
-        if (smem_once<MODE, E, CAP, true>() != cudaSuccess) return 0;
+        if (smem_once<MODE, E, CAP, true, STAGED>() != cudaSuccess) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(4);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = kSmem;
+        cfg.dynamicSmemBytes = smem_bytes(STAGED);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 4;
@@ -640,20 +764,20 @@ int quad_slots() {
         attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, loss_gemm_kernel<MODE, E, CAP, true>, &cfg) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, loss_gemm_kernel<MODE, E, CAP, true, STAGED>, &cfg) != cudaSuccess) n = 0;
         known[dev] = n + 1;
     }
     return known[dev] - 1;
 }
 
 // `across` tiles by `shared` ones that neighbours share an operand along.
-template <int MODE, bool E = false, bool CAP = false>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Work& w, int64_t across, int64_t shared,
-                   int num_sms, cudaStream_t stream) {
-    const int slots = shared > 1 ? quad_slots<MODE, E, CAP>() : 0;
-    const int64_t tiles = loss_cluster_tiles(int(across), int(shared), slots > 0);
-    if (slots > 0) return launch_clusters<MODE, E, CAP, true>(ta, tb, w, tiles < slots ? tiles : slots, stream);
-    return launch_clusters<MODE, E, CAP, false>(ta, tb, w, tiles < num_sms / 2 ? tiles : num_sms / 2, stream);
+template <int MODE, bool E = false, bool CAP = false, bool STAGED = false>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& to, const Work& w, int64_t across,
+                   int64_t shared, int num_sms, cudaStream_t stream) {
+    const int slots = shared > 1 ? quad_slots<MODE, E, CAP, STAGED>() : 0;
+    const int64_t tiles = loss_cluster_tiles(int(across), int(shared), slots > 0), pairs = num_sms / 2;
+    if (slots > 0) return launch_clusters<MODE, E, CAP, true, STAGED>(ta, tb, to, w, tiles < slots ? tiles : slots, stream);
+    return launch_clusters<MODE, E, CAP, false, STAGED>(ta, tb, to, w, tiles < pairs ? tiles : pairs, stream);
 }
 
 int64_t up(int64_t n, int64_t by) { return (n + by - 1) / by; }
@@ -667,10 +791,10 @@ cudaError_t loss_logits_launch(const LossGemmArgs& a, const uint16_t* h, int64_t
     const Work w{a, int(up(a.V, kTile))};
     const int64_t rows = up(a.rows, kTile);
     if (a.lm.cap > 0.f)
-        return a.e ? launch<LOGITS, true, true>(ta, tb, w, w.n_nt, rows, num_sms, stream)
-                   : launch<LOGITS, false, true>(ta, tb, w, w.n_nt, rows, num_sms, stream);
-    return a.e ? launch<LOGITS, true, false>(ta, tb, w, w.n_nt, rows, num_sms, stream)
-               : launch<LOGITS, false, false>(ta, tb, w, w.n_nt, rows, num_sms, stream);
+        return a.e ? launch<LOGITS, true, true>(ta, tb, tb, w, w.n_nt, rows, num_sms, stream)
+                   : launch<LOGITS, false, true>(ta, tb, tb, w, w.n_nt, rows, num_sms, stream);
+    return a.e ? launch<LOGITS, true, false>(ta, tb, tb, w, w.n_nt, rows, num_sms, stream)
+               : launch<LOGITS, false, false>(ta, tb, tb, w, w.n_nt, rows, num_sms, stream);
 }
 
 cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* W, int num_sms, LossDhGrid* grid,
@@ -679,14 +803,14 @@ cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 128) || !make_map(&tb, W, a.V, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
     bool quad = w.n_nt > 1;
-    int slots = quad ? quad_slots<DH, false, false>() : 0;
+    int slots = quad ? quad_slots<DH, false, false, false>() : 0;
     quad = slots > 0;
     if (!quad) slots = num_sms / 2;
     // a cluster for each part there can be: how many there are follows from the live rows
     const int64_t most = int64_t(loss_cluster_tiles(int(up(a.rows, kTile)), w.n_nt, quad)) * loss_split_limit(up(a.V, kStep));
     *grid = {w.n_nt, int(most < slots ? most : slots), quad};
-    return quad ? launch_clusters<DH, false, false, true>(ta, tb, w, grid->units, stream)
-                : launch_clusters<DH, false, false, false>(ta, tb, w, grid->units, stream);
+    return quad ? launch_clusters<DH, false, false, true, false>(ta, tb, tb, w, grid->units, stream)
+                : launch_clusters<DH, false, false, false, false>(ta, tb, tb, w, grid->units, stream);
 }
 
 cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t* h, int64_t h_rows, int num_sms,
@@ -694,7 +818,13 @@ cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     CUtensorMap ta, tb;
     if (!make_map(&ta, a.e, e_rows, a.V, a.e_ld, 64) || !make_map(&tb, h, h_rows, a.D, a.D, 64)) return cudaErrorInvalidValue;
     const Work w{a, int(up(a.D, kTile))};
-    return launch<DW>(ta, tb, w, up(a.V, kTile), w.n_nt, num_sms, stream);
+    const int64_t across = up(a.V, kTile);
+    if (a.first && a.last && up(a.rows, kStep) <= kStagedSteps) {
+        CUtensorMap to;
+        if (!make_map(&to, a.out, a.V, a.D, a.D, 32, !a.out_bf16)) return cudaErrorInvalidValue;
+        return launch<DW, false, false, true>(ta, tb, to, w, across, w.n_nt, num_sms, stream);
+    }
+    return launch<DW>(ta, tb, tb, w, across, w.n_nt, num_sms, stream);
 }
 
 }  // namespace df2
