@@ -35,9 +35,9 @@ namespace df2 {
 namespace {
 
 constexpr int kThreads = 640;
-// Registers: launched with 96 a thread; the first four warps keep 48 and the epilogue's sixteen
-// take 104 (128 * 48 + 512 * 104 <= 640 * 96).
-constexpr int kRoleRegisters = 48, kEpilogueRegisters = 104;
+// Registers: launched with 96 a thread; the first four warps keep 32 and the epilogue's sixteen
+// take 112 (128 * 32 + 512 * 112 = 640 * 96): what they spill goes to L2, the ring has the rest.
+constexpr int kRoleRegisters = 32, kEpilogueRegisters = 112;
 constexpr int kCols = kLossStats;              // columns of an epilogue thread
 constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
@@ -178,8 +178,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     const float inv_cap = CAP ? 1.f / cap : 0.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
-#pragma unroll 1
-    for (int c = 0; c < kCols; c += 32) {
+    auto columns = [&](int at, int c) {  // x[at .. at + 32), the row's columns from c on
 #pragma unroll
         for (int j0 = 0; j0 < 32; j0 += 16) {
             uint32_t word[8];
@@ -188,7 +187,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
                 float e[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float u = x[j0 + j + k], v = CAP ? map(u) : u;
+                    const float u = x[at + j0 + j + k], v = CAP ? map(u) : u;
                     e[k] = exp2_fast(__fmul_rn(__fsub_rn(v, base), by));
                     if (CAP && u == -INFINITY) e[k] = 0.f;
                     sum[(j + k) & 3] = __fadd_rn(sum[(j + k) & 3], e[k]);
@@ -199,7 +198,16 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
             }
             if (E) store8(out + c + j0, word, true);
         }
-        turn(x);
+    };
+    if (CAP) {
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 32) {
+            columns(0, c);
+            turn(x);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) columns(c, c);
     }
     a.stats[int64_t(row) * a.n_stats + nt * (kTile / kCols) + part] =
         make_float2(none ? top : CAP ? base : __fmul_rn(top, mul), (sum[0] + sum[1]) + (sum[2] + sum[3]));

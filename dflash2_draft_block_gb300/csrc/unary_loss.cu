@@ -80,19 +80,18 @@ live_rows_kernel(const LossRowsArgs a, const int each) {
         }
     }
     __syncthreads();
-    const int units = int(a.D / 8);  // of 16 bytes of bf16
-    const int dh_units = a.dh ? units * (a.dh_bf16 ? 1 : 2) : 0;
-    for (int64_t p = first; p < last; ++p) {
-        const int at = place[p - first];
-        if (at >= 0) {
-            const uint4* from = reinterpret_cast<const uint4*>(a.h + p * a.D);
-            uint4* to = reinterpret_cast<uint4*>(a.live_h + int64_t(at) * a.D);
-            for (int u = threadIdx.x; u < units; u += kThreads) to[u] = __ldcs(from + u);
-        } else {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<char*>(a.dh) + p * dh_units * 16);
-            for (int u = threadIdx.x; u < dh_units; u += kThreads) to[u] = make_uint4(0u, 0u, 0u, 0u);
-        }
+    // 16 bytes of bf16 a unit; the block's rows are one run of units
+    const int units = int(a.D / 8), rows = int(last - first);
+    for (int u = threadIdx.x; u < rows * units; u += kThreads) {
+        const int r = u / units, at = place[r];
+        if (at >= 0)
+            reinterpret_cast<uint4*>(a.live_h + int64_t(at) * a.D)[u - r * units] =
+                __ldcs(reinterpret_cast<const uint4*>(a.h + first * a.D) + u);
     }
+    const int dh_units = a.dh ? units * (a.dh_bf16 ? 1 : 2) : 0;
+    for (int u = threadIdx.x; u < rows * dh_units; u += kThreads)
+        if (place[u / dh_units] < 0)
+            reinterpret_cast<uint4*>(static_cast<char*>(a.dh) + first * dh_units * 16)[u] = make_uint4(0u, 0u, 0u, 0u);
     if (last == a.P) {  // rows of the last K step of dW's product
         const int64_t total = so_far, end = (total + 63) / 64 * 64;
         uint4* to = reinterpret_cast<uint4*>(a.live_h + total * a.D);
@@ -232,8 +231,11 @@ cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, cudaStream_t stre
 }  // namespace
 
 cudaError_t loss_rows_launch(const LossRowsArgs& a, cudaStream_t stream) {
-    // a row a block, or more of them where the blocks' own counting would be the longer part
-    int64_t each = (a.P + 4095) / 4096;
+    // a row a block, or more of them where they are short or the blocks' own counting would be
+    // the longer part
+    int64_t each = (a.P + 4095) / 4096, full = 4096 / a.D;
+    if (full > 32) full = 32;
+    if (each < full) each = full;
     if (each > kThreads) each = kThreads;
     const int64_t grid = (a.P + each - 1) / each;
     live_rows_kernel<<<unsigned(grid), kThreads, 0, stream>>>(a, int(each));
