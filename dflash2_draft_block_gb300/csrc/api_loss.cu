@@ -42,7 +42,7 @@ struct Plan {
     size_t count, map, targets, target_logit, h, stats, e, part, sums, bytes;
 };
 
-Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
+Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
     Plan p{};
     const bool grads = dh || dw;
     p.h_rows = up(P, 64);
@@ -68,9 +68,10 @@ Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
     p.h = take(size_t(p.h_rows) * D * 2);
     p.stats = take(size_t(p.rows) * p.n_stats * 8);
     p.e = take(grads ? size_t(p.e_rows) * p.e_ld * 2 : 0);
-    const int64_t splits = dh ? df2::loss_split_limit((V + 63) / 64) : 1;
-    const int64_t partial = splits > 1 ? splits * p.rows * D : 0;
-    p.part = take(size_t(partial < df2::kLossPartial ? partial : df2::kLossPartial) * 4);
+    // parts of 256 x 256 sums: a cluster's share of them, or all that there can be
+    const int64_t ways = dh ? df2::loss_way_limit((V + 63) / 64) : 1;
+    const int64_t some = df2::kLossPartTiles * (num_sms / 2), all = up(p.rows, 256) / 256 * (up(D, 512) / 256) * ways;
+    p.part = take(ways > 1 ? size_t(some < all ? some : all) * 65536 * 4 : 0);
     p.sums = take(dw && p.pieces > 1 ? size_t(V) * D * 4 : 0);
     p.bytes = at;
     return p;
@@ -156,7 +157,7 @@ cudaError_t run(const Call& c, const Plan& p, int num_sms) {
             g.part = reinterpret_cast<float*>(c.ws + p.part);
             df2::LossDhGrid grid{};
             e = df2::loss_dh_launch(g, p.e_rows, c.W, num_sms, &grid, c.stream);
-            if (e == cudaSuccess && df2::loss_split_limit((c.V + 63) / 64) > 1)
+            if (e == cudaSuccess && df2::loss_way_limit((c.V + 63) / 64) > 1)
                 e = df2::loss_sum_parts_launch(g, grid, c.stream);
             if (e != cudaSuccess) break;
         }
@@ -204,7 +205,7 @@ int call(Call c, float multiplier, float cap, void* workspace, size_t workspace_
     }
     const int sms = num_sms_current();
     if (sms < 2) return DF2_ERR_CUDA;
-    const Plan p = make_plan(c.P, c.D, c.V, c.dh, c.dw);
+    const Plan p = make_plan(c.P, c.D, c.V, c.dh, c.dw, sms);
     if (workspace_bytes < p.bytes || !workspace) return DF2_ERR_WORKSPACE_TOO_SMALL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255u) return DF2_ERR_UNSUPPORTED;
     c.ws = static_cast<char*>(workspace);
@@ -213,7 +214,8 @@ int call(Call c, float multiplier, float cap, void* workspace, size_t workspace_
 
 size_t workspace_size(int64_t P, int64_t D, int64_t V, bool dh, bool dw) {
     if (check_shape(P, D, V) != DF2_OK || P == 0) return 0;
-    return make_plan(P, D, V, dh, dw).bytes;
+    const int sms = num_sms_current();
+    return make_plan(P, D, V, dh, dw, sms < 2 ? 152 : sms).bytes;
 }
 
 }  // namespace

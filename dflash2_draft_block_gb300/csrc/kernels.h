@@ -182,7 +182,8 @@ struct LossGemmArgs {
     LogitMap lm;
     uint16_t* e;              // [rows, e_ld], nullable
     int64_t e_ld;
-    // the gradients: dh rows by map, or their parts [splits, live rows, D]; dW
+    // the gradients: dh rows by map, or the parts of tiles that are cut, of 256 x 256 (LossTile.part; a
+    // quad's two after each other); dW
     void* out;
     bool out_bf16;
     float* part;
@@ -190,18 +191,19 @@ struct LossGemmArgs {
     bool first, last, accumulate;
 };
 
-// The split of dh's product (loss_tiles.h), by a whole warp.
-__device__ __forceinline__ int loss_splits(int64_t tiles, int64_t steps, int64_t units, int64_t rows, int64_t D, int lane) {
+// How `units` clusters share the tiles of dh's product (loss_tiles.h), by a whole warp.
+__device__ __forceinline__ LossSplit loss_split(int tiles, int64_t steps, int units, bool quad, int lane) {
+    const int rest = tiles % units;
     int64_t best = INT64_MAX;
-    for (int s = lane + 1; s <= loss_split_limit(steps); s += 32) {
-        const int64_t key = loss_split_key(s, tiles, steps, units, rows, D);
+    for (int s = lane + 1; s <= loss_way_limit(steps); s += 32) {
+        const int64_t key = loss_way_key(s, rest, steps, units, quad);
         best = key < best ? key : best;
     }
     for (int o = 16; o; o >>= 1) {
         const int64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, o);
         best = other < best ? other : best;
     }
-    return int(best & 127);
+    return LossSplit{tiles - rest, rest, int(best & 127)};
 }
 struct LossDhGrid {
     int n_nt, units;          // N tiles, clusters

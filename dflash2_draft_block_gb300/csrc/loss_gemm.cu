@@ -427,10 +427,10 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     const int units = int(gridDim.x) / (2 * kPairs), unit = int(blockIdx.x) / (2 * kPairs);
     const int n_nt = w.n_nt;
     const int tiles = MODE == LOGITS ? loss_cluster_tiles(n_nt, n_mu, QUAD) : loss_cluster_tiles(n_mu, n_nt, QUAD);
-    const int splits = MODE == DH ? loss_splits(tiles, k_total, units, live, a.D, lane) : 1;
-    const int total = tiles * splits;
+    const LossSplit work = MODE == DH ? loss_split(tiles, k_total, units, QUAD, lane) : LossSplit{tiles, 0, 1};
+    const int total = work.items();
 
-    auto tile = [&](int i) { return loss_tile<MODE == LOGITS, QUAD>(i, n_mu, n_nt, splits, k_total, which); };
+    auto tile = [&](int i) { return loss_tile<MODE == LOGITS, QUAD>(i, n_mu, n_nt, work, k_total, which); };
 
     const int segment = MODE == DW ? max(k_total, 1) : kSegment;
     if (warp < 4) {
@@ -661,13 +661,11 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 } else {
                     const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
                     if (m < live && n > 0) {
-                        if (splits > 1) {
-                            write_row<false>(x, n, a.part + (int64_t(t.split) * live + m) * a.D + n0);
-                        } else {
-                            const int64_t o = int64_t(a.map[a.row0 + m]) * a.D + n0;
-                            if (a.out_bf16) write_row<true>(x, n, static_cast<uint16_t*>(a.out) + o);
-                            else write_row<false>(x, n, static_cast<float*>(a.out) + o);
-                        }
+                        const int64_t o = t.part < 0 ? int64_t(a.map[a.row0 + m]) * a.D + n0
+                                                     : (int64_t(t.part * kPairs + which) * kTile + (m - t.mu * kTile)) * kTile +
+                                                           part * kCols;
+                        if (t.part < 0 && a.out_bf16) write_row<true>(x, n, static_cast<uint16_t*>(a.out) + o);
+                        else write_row<false>(x, n, (t.part < 0 ? static_cast<float*>(a.out) : a.part) + o);
                     }
                     __syncwarp();
                 }
@@ -815,7 +813,7 @@ cudaError_t loss_dh_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
     quad = slots > 0;
     if (!quad) slots = num_sms / 2;
     // a cluster for each part there can be: how many there are follows from the live rows
-    const int64_t most = int64_t(loss_cluster_tiles(int(up(a.rows, kTile)), w.n_nt, quad)) * loss_split_limit(up(a.V, kStep));
+    const int64_t most = int64_t(loss_cluster_tiles(int(up(a.rows, kTile)), w.n_nt, quad)) * loss_way_limit(up(a.V, kStep));
     *grid = {w.n_nt, int(most < slots ? most : slots), quad};
     return quad ? launch_clusters<DH, false, false, true, false>(ta, tb, tb, w, grid->units, stream)
                 : launch_clusters<DH, false, false, false, false>(ta, tb, tb, w, grid->units, stream);

@@ -17,22 +17,28 @@ __host__ __device__ inline int loss_cluster_tiles(int across, int shared, bool q
 
 struct LossTile {
     int mu, nt;     // M unit and N tile, of 256 each; either may be one past the end in a quad
-    int split;
+    int part;       // -1: the whole sum; else the place of this part of it among the parts
     int k0, k1;     // K steps
     bool alone;     // the pairs of a cluster share nothing
 };
 
-// Tile i of the clusters' tiles * splits, for pair `which` of the cluster.  LOGITS (h W^T): M fastest
-// in groups, so that W streams past while a group's rows of h stay in L2; quads take two M units.
-// The gradients: N fastest, so that the clusters of a moment share g's rows; quads take two N
-// tiles.
+// The clusters' work: `whole` tiles, then `rest` tiles in `ways` parts each (1: whole, too).
+struct LossSplit {
+    int whole, rest, ways;
+    __host__ __device__ int items() const { return whole + rest * ways; }
+};
+
+// Item i of them, for pair `which` of the cluster.  LOGITS (h W^T): M fastest in groups, so that W
+// streams past while a group's rows of h stay in L2; quads take two M units.  The gradients: N
+// fastest, so that the clusters of a moment share g's rows; quads take two N tiles.
 template <bool LOGITS, bool QUAD>
-__host__ __device__ inline LossTile loss_tile(int i, int n_mu, int n_nt, int splits, int k_total, int which) {
+__host__ __device__ inline LossTile loss_tile(int i, int n_mu, int n_nt, const LossSplit& work, int k_total, int which) {
     constexpr int kPairs = QUAD ? 2 : 1;
-    const int tiles = LOGITS ? loss_cluster_tiles(n_nt, n_mu, QUAD) : loss_cluster_tiles(n_mu, n_nt, QUAD);
     LossTile t;
-    t.split = i / tiles;
-    const int j = i - t.split * tiles;
+    const bool split = work.ways > 1 && i >= work.whole;
+    t.part = split ? i - work.whole : -1;  // the parts of a kind together, of all tiles
+    const int kind = split ? t.part / work.rest : 0;
+    const int j = split ? i - kind * work.rest : i;
     t.alone = false;
     if (LOGITS) {
         constexpr int kRun = kLossGroup / kPairs;
@@ -58,28 +64,28 @@ __host__ __device__ inline LossTile loss_tile(int i, int n_mu, int n_nt, int spl
             t.alone = true;
         }
     }
-    t.k0 = int(int64_t(k_total) * t.split / splits);
-    t.k1 = int(int64_t(k_total) * (t.split + 1) / splits);
+    t.k0 = split ? int(int64_t(k_total) * kind / work.ways) : 0;
+    t.k1 = split ? int(int64_t(k_total) * (kind + 1) / work.ways) : k_total;
     return t;
 }
 
-// How many ways dh's product is split along V, for `tiles` tiles of `steps` steps (of 64) on
-// `units` clusters: the busiest cluster's steps at 0.3 us, and the partial sums' way out and
-// back at 4 TB/s, in ns.  The live rows decide, so it is worked out on the device, by each
-// kernel that needs it; in whole numbers, so that all find the same.
-constexpr int kLossSplits = 64;
-constexpr int64_t kLossPartial = int64_t(1) << 27;  // fp32 sums held at most
-__host__ __device__ inline int loss_split_limit(int64_t steps) {
+// dh's product has few tiles and long sums (of V): its tiles go to the clusters whole as long as
+// that fills rounds of all of them, and what is left over is cut along V.  Into how many parts:
+// the busiest cluster's steps (of 64) at 0.3 us, and the parts' way out and back at 4 TB/s, in
+// ns.  The live rows decide, so it is worked out on the device, by each kernel that needs it;
+// in whole numbers, so that all find the same.
+constexpr int kLossWays = 64;        // parts of a tile at most
+constexpr int kLossPartTiles = 8;    // parts a cluster at most, on average
+__host__ __device__ inline int loss_way_limit(int64_t steps) {
     const int64_t s = (steps + 3) / 4;
-    return int(s < kLossSplits ? s : kLossSplits);
+    return int(s < kLossWays ? s : kLossWays);
 }
-// s ways, as a key whose least is the best: the time, and of equal ones the fewer ways.
-__host__ __device__ inline int64_t loss_split_key(int s, int64_t tiles, int64_t steps, int64_t units, int64_t rows,
-                                                  int64_t D) {
-    if (s > 1 && s * rows * D > kLossPartial) return INT64_MAX;
-    int64_t ns = (tiles * s + units - 1) / units * ((steps + s - 1) / s) * 300;
-    if (s > 1) ns += 3000 + s * rows * D * 2 / 1000;
-    return ns * 128 + s;
+// `ways` ways, as a key whose least is the best: the time, and of equal ones the fewer ways.
+__host__ __device__ inline int64_t loss_way_key(int ways, int64_t rest, int64_t steps, int64_t units, bool quad) {
+    if (ways > 1 && ways * rest > kLossPartTiles * units) return INT64_MAX;
+    int64_t ns = (rest * ways + units - 1) / units * ((steps + ways - 1) / ways) * 300;
+    if (ways > 1) ns += 3000 + ways * rest * (quad ? 262 : 131);
+    return ns * 128 + ways;
 }
 
 }  // namespace df2

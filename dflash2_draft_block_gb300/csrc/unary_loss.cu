@@ -9,7 +9,7 @@
 //   live_rows_kernel   the rows that have a target, in order, copied next to each other: the
 //                      products neither compute the others nor meet a NaN in them
 //   row_loss_kernel    a row's loss from its tiles' statistics, and its e to g in place
-//   sum_parts_kernel   dh from the K splits' partial sums, in order
+//   sum_parts_kernel   the rows of dh whose sums were cut, from their parts in order
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -170,43 +170,54 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
     }
 }
 
-// A thread sums 4 columns of a row.
+// grid (tiles that can be cut, pairs' tiles of each, 8 rows of a tile): the sums of a tile's parts,
+// in order.
+template <bool QUAD>
 __global__ void __launch_bounds__(kThreads)
 sum_parts_kernel(const int32_t* count, int64_t row0, int rows, const int32_t* map, const float* part, int64_t V,
                  int64_t D, LossDhGrid grid, void* dh, bool bf16) {
-    __shared__ int shared_splits;
+    __shared__ LossSplit shared;
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t left = int64_t(*count) - row0;
-    const int64_t live = left < 0 ? 0 : left > rows ? rows : left;
-    const int64_t row = blockIdx.x;
-    if (row >= live) return;
+    const int live = int(left < 0 ? 0 : left > rows ? rows : left);
+    const int n_mu = (live + 255) / 256, steps = int((V + 63) / 64);
     if (threadIdx.x < 32) {
-        const int tiles = loss_cluster_tiles(int((live + 255) / 256), grid.n_nt, grid.quad);
-        const int splits = loss_splits(tiles, (V + 63) / 64, grid.units, live, D, threadIdx.x);
-        if (threadIdx.x == 0) shared_splits = splits;
+        const LossSplit work = loss_split(loss_cluster_tiles(n_mu, grid.n_nt, QUAD), steps, grid.units, QUAD, threadIdx.x);
+        if (threadIdx.x == 0) shared = work;
     }
     __syncthreads();
-    const int splits = shared_splits;
-    if (splits == 1) return;  // the product wrote dh itself
-    const int64_t p = map[row0 + row];
-    for (int64_t d = 4 * (int64_t(blockIdx.y) * kThreads + threadIdx.x); d < D; d += 4 * int64_t(gridDim.y) * kThreads) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float* from = part + row * D + d;
+    const LossSplit work = shared;
+    const int tile = blockIdx.x, which = blockIdx.y;
+    if (work.ways == 1 || tile >= work.rest) return;  // the product wrote dh itself
+    const LossTile t = loss_tile<false, QUAD>(work.whole + tile, n_mu, grid.n_nt, work, steps, which);
+    constexpr int kPairs = QUAD ? 2 : 1;
+    const int64_t d = int64_t(t.nt) * 256 + (threadIdx.x & 31) * 8;
+    if (d >= D) return;
+    const int r = blockIdx.z * 8 + threadIdx.x / 32, m = t.mu * 256 + r;
+    if (m >= live) return;
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const float* from = part + ((int64_t(tile) * kPairs + which) * 256 + r) * 256 + (threadIdx.x & 31) * 8;
 #pragma unroll 4
-        for (int k = 0; k < splits; ++k) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(from + k * live * D));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
-        if (bf16) {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(dh) + p * D + d) =
-                make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-        } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(dh) + p * D + d) = s;
-        }
+    for (int k = 0; k < work.ways; ++k, from += int64_t(work.rest) * kPairs * 65536) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(from)), w = __ldcs(reinterpret_cast<const float4*>(from) + 1);
+        f[0] += v.x;
+        f[1] += v.y;
+        f[2] += v.z;
+        f[3] += v.w;
+        f[4] += w.x;
+        f[5] += w.y;
+        f[6] += w.z;
+        f[7] += w.w;
+    }
+    const int64_t o = int64_t(map[row0 + m]) * D + d;
+    if (bf16) {
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dh) + o) =
+            make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+    } else {
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(dh) + o);
+        to[0] = make_float4(f[0], f[1], f[2], f[3]);
+        to[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
 }
 
@@ -257,9 +268,14 @@ cudaError_t loss_row_launch(const LossRowArgs& a, int64_t e_rows, int num_sms, c
 }
 
 cudaError_t loss_sum_parts_launch(const LossGemmArgs& a, const LossDhGrid& grid, cudaStream_t stream) {
-    const int64_t across = (a.D + 4 * kThreads - 1) / (4 * kThreads);
-    return launch_after(sum_parts_kernel, dim3(unsigned(a.rows), unsigned(across < 64 ? across : 64)), stream, a.count,
-                        a.row0, a.rows, a.map, static_cast<const float*>(a.part), a.V, a.D, grid, a.out, a.out_bf16);
+    // at most as many tiles are left over as there are clusters, less one, or tiles at all
+    const int tiles = loss_cluster_tiles(int((a.rows + 255) / 256), grid.n_nt, grid.quad);
+    const dim3 blocks(unsigned(tiles < grid.units ? tiles : grid.units), grid.quad ? 2 : 1, 32);
+    const float* part = a.part;
+    return grid.quad ? launch_after(sum_parts_kernel<true>, blocks, stream, a.count, a.row0, a.rows, a.map, part, a.V, a.D,
+                                    grid, a.out, a.out_bf16)
+                     : launch_after(sum_parts_kernel<false>, blocks, stream, a.count, a.row0, a.rows, a.map, part, a.V, a.D,
+                                    grid, a.out, a.out_bf16);
 }
 
 }  // namespace df2

@@ -19,18 +19,30 @@ CODE = r"""
 #define __device__
 #include "loss_tiles.h"
 using namespace df2;
-// 0: every tile and K step once; counts: [n_mu][n_nt][k_total] bytes of scratch
+// 0: every tile and K step once, and the parts of a tile where their sum looks for them; counts:
+// [n_mu][n_nt][k_total] bytes of scratch
 template <bool L, bool Q>
-static int sweep(int n_mu, int n_nt, int splits, int k_total, uint8_t* counts) {
+static int sweep(int n_mu, int n_nt, int rest, int ways, int k_total, uint8_t* counts) {
     const int pairs = Q ? 2 : 1;
     const int tiles = L ? loss_cluster_tiles(n_nt, n_mu, Q) : loss_cluster_tiles(n_mu, n_nt, Q);
+    if (rest > tiles) rest = tiles;
+    const LossSplit work{tiles - rest, rest, ways};
     std::memset(counts, 0, size_t(n_mu) * n_nt * k_total);
-    for (int i = 0; i < tiles * splits; ++i) {
+    if (work.items() != tiles - rest + rest * ways) return 8;
+    for (int i = 0; i < work.items(); ++i) {
         LossTile t[2];
         for (int q = 0; q < pairs; ++q) {
-            t[q] = loss_tile<L, Q>(i, n_mu, n_nt, splits, k_total, q);
+            t[q] = loss_tile<L, Q>(i, n_mu, n_nt, work, k_total, q);
             if (t[q].mu < 0 || t[q].nt < 0 || t[q].mu > n_mu || t[q].nt > n_nt) return 1;
             if (t[q].k0 < 0 || t[q].k1 > k_total || t[q].k0 > t[q].k1) return 2;
+            const bool split = ways > 1 && i >= work.whole;
+            if (!split && (t[q].part != -1 || t[q].k0 != 0 || t[q].k1 != k_total)) return 9;
+            if (split) {
+                const int tile = t[q].part % rest;  // the part's tile, and the whole one that its sum is
+                const LossTile w = loss_tile<L, Q>(work.whole + tile, n_mu, n_nt, work, k_total, q);
+                if (t[q].part < 0 || t[q].part >= rest * ways || w.mu != t[q].mu || w.nt != t[q].nt) return 10;
+                if (t[q].k0 == t[q].k1) return 11;
+            }
             if (t[q].mu >= n_mu || t[q].nt >= n_nt) {
                 if (!Q || q != 1 || !t[q].alone) return 3;
                 continue;
@@ -38,7 +50,7 @@ static int sweep(int n_mu, int n_nt, int splits, int k_total, uint8_t* counts) {
             for (int k = t[q].k0; k < t[q].k1; ++k) ++counts[(size_t(t[q].mu) * n_nt + t[q].nt) * k_total + k];
         }
         if (Q) {  // one list of K steps, and the shared operand where there is one
-            if (t[0].alone != t[1].alone || t[0].k0 != t[1].k0 || t[0].k1 != t[1].k1) return 4;
+            if (t[0].alone != t[1].alone || t[0].k0 != t[1].k0 || t[0].k1 != t[1].k1 || t[0].part != t[1].part) return 4;
             if (!t[0].alone && (L ? t[0].nt != t[1].nt : t[0].mu != t[1].mu)) return 5;
         } else if (t[0].alone) {
             return 6;
@@ -48,15 +60,15 @@ static int sweep(int n_mu, int n_nt, int splits, int k_total, uint8_t* counts) {
         if (counts[i] != 1) return 7;
     return 0;
 }
-extern "C" int sweep_tiles(int logits, int quad, int n_mu, int n_nt, int splits, int k_total, uint8_t* counts) {
-    if (logits) return quad ? sweep<true, true>(n_mu, n_nt, splits, k_total, counts) : sweep<true, false>(n_mu, n_nt, splits, k_total, counts);
-    return quad ? sweep<false, true>(n_mu, n_nt, splits, k_total, counts) : sweep<false, false>(n_mu, n_nt, splits, k_total, counts);
+extern "C" int sweep_tiles(int logits, int quad, int n_mu, int n_nt, int rest, int ways, int k_total, uint8_t* counts) {
+    if (logits) return quad ? sweep<true, true>(n_mu, n_nt, rest, ways, k_total, counts) : sweep<true, false>(n_mu, n_nt, rest, ways, k_total, counts);
+    return quad ? sweep<false, true>(n_mu, n_nt, rest, ways, k_total, counts) : sweep<false, false>(n_mu, n_nt, rest, ways, k_total, counts);
 }
-extern "C" int64_t split_key(int s, int64_t tiles, int64_t steps, int64_t units, int64_t rows, int64_t D) {
-    return loss_split_key(s, tiles, steps, units, rows, D);
+extern "C" int64_t way_key(int ways, int64_t rest, int64_t steps, int64_t units, int quad) {
+    return loss_way_key(ways, rest, steps, units, quad != 0);
 }
-extern "C" int split_limit(int64_t steps) { return loss_split_limit(steps); }
-extern "C" int64_t partial_limit() { return kLossPartial; }
+extern "C" int way_limit(int64_t steps) { return loss_way_limit(steps); }
+extern "C" int part_tiles() { return kLossPartTiles; }
 """
 
 
@@ -70,9 +82,9 @@ def lib(tmp_path_factory):
     subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", "-I", CSRC, str(d / "t.cpp"), "-o",
                     str(d / "t.so")], check=True)
     lib = ctypes.CDLL(str(d / "t.so"))
-    lib.split_key.restype = lib.partial_limit.restype = ctypes.c_int64
-    lib.split_key.argtypes = [ctypes.c_int] + [ctypes.c_int64] * 5
-    lib.split_limit.argtypes = [ctypes.c_int64]
+    lib.way_key.restype = ctypes.c_int64
+    lib.way_key.argtypes = [ctypes.c_int] + [ctypes.c_int64] * 3 + [ctypes.c_int]
+    lib.way_limit.argtypes = [ctypes.c_int64]
     return lib
 
 
@@ -83,24 +95,25 @@ def test_every_tile_once(lib):
     counts = (ctypes.c_uint8 * (70 * 100 * 64))()
     for m, n in shapes:
         for quad in (0, 1):
-            assert lib.sweep_tiles(1, quad, m, n, 1, 3, counts) == 0, (m, n, quad)
-            for splits, steps in ((1, 1), (1, 5), (3, 7), (5, 5), (8, 50)):
+            assert lib.sweep_tiles(1, quad, m, n, 0, 1, 3, counts) == 0, (m, n, quad)
+            for rest, ways, steps in ((0, 1, 1), (9, 1, 5), (1, 3, 7), (7, 5, 5), (35, 8, 50), (9999, 4, 16)):
                 if m * n * steps < 70 * 100 * 64:
-                    assert lib.sweep_tiles(0, quad, m, n, splits, steps, counts) == 0, (m, n, quad, splits, steps)
+                    assert lib.sweep_tiles(0, quad, m, n, rest, ways, steps, counts) == 0, (m, n, quad, rest, ways, steps)
 
 
-def test_splits(lib):
+def test_ways(lib):
+    """The parts fit their space, none is empty, and with one part to a cluster and round nothing is cut."""
     rng = random.Random(2)
     none = (1 << 63) - 1
     for _ in range(3000):
-        rows, D, V = rng.randint(1, 20000), 8 * rng.randint(1, 1000), rng.randint(1, 300000)
-        steps, units = (V + 63) // 64, rng.choice([36, 76])
-        tiles = -(-rows // 256) * -(-D // 256)
-        limit = lib.split_limit(steps)
+        units, quad = rng.choice([(36, 1), (76, 0)])
+        steps, rest = rng.randint(1, 5000), rng.randint(0, units - 1)
+        limit = lib.way_limit(steps)
         assert 1 <= limit <= min(64, max(1, (steps + 3) // 4))
-        keys = {s: lib.split_key(s, tiles, steps, units, rows, D) for s in range(1, limit + 1)}
+        keys = {s: lib.way_key(s, rest, steps, units, quad) for s in range(1, limit + 1)}
         best = min(keys.values())
         s = best & 127
-        assert best != none and keys[s] == best and 1 <= s <= limit
-        assert s == 1 or s * rows * D <= lib.partial_limit()
-        assert s <= steps  # no part is empty
+        assert best != none and keys[s] == best and 1 <= s <= limit <= steps + 3
+        assert s == 1 or s * rest <= lib.part_tiles() * units
+        assert s <= steps
+        assert rest or s == 1
