@@ -12,6 +12,8 @@ do, and gradients come from the *_grad calls.
     loss, label = selector_ce(s, ids, targets, V)      # the selector's K-way CE
     y, dyn = conv_prepare(x, block_size, taps, group, W_proj, base)
     y2 = conv_finish(z, block_size, taps, group, dyn, base)
+    loss, lse, dh, dW = unary_loss_grad(h, W_lm, targets)  # full-vocabulary CE, gradients
+    y = dropout(x, rate, seed, step)                    # dropout_grad: the same mask
 """
 from __future__ import annotations
 
