@@ -481,17 +481,17 @@ int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int6
  * The logits are never stored.  Products are of the bf16 inputs; sums, maxima and the loss
  * are fp32, and the loss of a row that is all but certain of its target does not cancel.
  * A row without a target (targets[p] < 0) gives NaN in both and is not computed (its h may
- * hold anything); a target >= V does the same and sets DF2_STATUS_ID_OUT_OF_RANGE.  A NaN or
- * infinity in another row's h reaches that row's loss, and no other.
+ * hold anything); a target >= V does the same and sets DF2_STATUS_ID_OUT_OF_RANGE.  A NaN in
+ * another row's h reaches that row's loss, and no other.
  *
  *   h [P, D] bf16; W_lm [V, D] bf16; targets [P] int32
  *   loss [P] fp32 out; lse [P] fp32 out, nullable
  *   workspace >= dflash2_unary_ce_workspace_size(P, D, V): a copy of h and at most 1 GiB of
  *             statistics of 64 columns each (more rows go in pieces), or 256 rows' where those
  *             are more
- * Rules: P >= 0, V >= 1, D >= 1, D % 8 == 0; output_multiplier and final_logit_softcapping as
- * dflash2_unary_topk; P <= 2^20, V <= 2^24, D <= 2^20 (else DF2_ERR_UNSUPPORTED); outputs must
- * not overlap inputs or one another.  h and W_lm 16-byte aligned, the rest by their elements.
+ * Rules: P >= 0, V >= 1, D >= 1, D % 8 == 0; output_multiplier m and final_logit_softcapping c as
+ * dflash2_unary_topk; P <= 2^20, V <= 2^24, D <= 2^20, 1 / c and m / c finite in fp32 (else
+ * DF2_ERR_UNSUPPORTED); outputs must not overlap inputs or one another.  h and W_lm 16-byte aligned, the rest by their elements.
  * ---------------------------------------------------------------------- */
 size_t dflash2_unary_ce_workspace_size(int64_t P, int64_t D, int64_t V);
 int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_lm, int64_t V,

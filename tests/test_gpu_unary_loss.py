@@ -233,6 +233,47 @@ def test_more_than_one_piece(df2):
         torch.cuda.empty_cache()
 
 
+def test_offsets_past_32_bits(df2):
+    """A head of 2.46e9 elements: logits, dh and the ends of dW, in fp32 and added in bf16, against sums in
+    64 bits a piece of the head at a time."""
+    V, D, P = 600_000, 4096, 8
+    g = torch.Generator(device="cuda").manual_seed(40)
+    W = torch.empty(V, D, dtype=BF, device="cuda").normal_(0.0, 0.04, generator=g)
+    h = torch.randn(P, D, generator=g, device="cuda").to(BF)
+    t = torch.tensor([0, 1, 299_999, 524_288, 599_998, 599_999, -1, 400_000], dtype=I32, device="cuda")
+    live = t >= 0
+    x, S = [], []
+    for w in W.split(50_000):
+        x.append(h.double() @ w.double().T)
+        S.append(h.double().abs() @ w.double().abs().T)
+    x, du = torch.cat(x, 1), (D / 16 + 4) * 2.0 ** -23 * torch.cat(S, 1)
+    lse = torch.logsumexp(x, 1)
+    gr = torch.exp(x - lse[:, None])
+    gr[torch.arange(P, device="cuda"), t.long().clamp(min=0)] -= 1.0
+    gr[~live] = 0.0
+    # a factor: its logit's and the log-sum-exp's errors, exp's and the sums', fp16 and bf16
+    dg = gr.abs() * (2 * du.amax(1, keepdim=True) + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -15) + 2.0 ** -36
+    want, room = torch.zeros(P, D, dtype=torch.float64, device="cuda"), torch.zeros(P, D, dtype=torch.float64, device="cuda")
+    for k, w in enumerate(W.split(50_000)):
+        part = slice(50_000 * k, 50_000 * k + len(w))
+        want += gr[:, part] @ w.double()
+        room += (dg[:, part] + (V / 16 + 4) * 2.0 ** -23 * gr[:, part].abs()) @ w.double().abs()
+    rows = torch.cat([torch.arange(0, 64), torch.arange(299_990, 300_010), torch.arange(524_280, 524_300),
+                      torch.arange(V - 64, V)]).cuda()
+    wW, rW = gr[:, rows].T @ h.double(), dg[:, rows].T @ h.double().abs()
+    dW = torch.full((V, D), 0.5, dtype=BF, device="cuda")
+    for more in (dict(dW=True, dtype=F32), dict(dW=dW, accumulate=True)):
+        loss, l, dh, got = df2.unary_loss_grad(h, W, t, **more)
+        assert bool(((l - lse).abs()[live] <= du.amax(1)[live] + 2.0 ** -17).all()) and bool(l[~live].isnan().all())
+        xt = x[torch.arange(P, device="cuda"), t.long().clamp(min=0)]
+        assert bool(((loss - (lse - xt)).abs()[live] <= 2 * du.amax(1)[live] + 2.0 ** -17).all())
+        check("dh", dh, want, room)
+        had = 0.5 if "accumulate" in more else 0.0
+        check("dW", got[rows], wW + had, rW + 2.0 ** -22 * (wW.abs() + had))
+        del got
+        torch.cuda.empty_cache()
+
+
 def test_zero_rows(df2):
     h, W, t, w = inputs(19, 4, 100, 64)
     loss, lse, dh, dW = df2.unary_loss_grad(h[:0], W, t[:0], dW=torch.ones(100, 64, device="cuda"))

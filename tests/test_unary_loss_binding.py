@@ -135,7 +135,7 @@ def test_library_refusals():
         assert call(**bad) == 1, bad
     for bad in (dict(D=20), dict(P=(1 << 20) + 1), dict(D=(1 << 20) + 8), dict(V=(1 << 24) + 1), dict(h=base + 8), dict(W=2 * base + 2),
                 dict(dh=6 * base + 8), dict(dW=7 * base + 4), dict(t=3 * base + 2), dict(loss=4 * base + 1),
-                dict(lse=5 * base + 2), dict(w=9 * base + 1)):
+                dict(lse=5 * base + 2), dict(w=9 * base + 1), dict(cap=1e-40), dict(cap=1e-20, mul=1e20)):
         assert call(**bad) == 2, bad
     assert call(P=0, acc=1) == 0 and call(P=0, dW=0) == 0
 
