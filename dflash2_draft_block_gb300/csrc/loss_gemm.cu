@@ -148,9 +148,10 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&w)[8], bool wid
 // units of 2^-15 (11 bits of exp(x - M) down to M - 20, then fewer until M - 27; bf16 here and
 // again as g would double the factors' rounding error).
 template <bool E, bool CAP>
-__device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[kCols], int row, int nt, int part) {
+__device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[kCols], int row, int target, int nt,
+                                                int part) {
     const int64_t c0 = int64_t(nt) * kTile + part * kCols;
-    const int64_t t = a.targets[a.row0 + row] - c0;
+    const int64_t t = target - c0;
     const float cap = a.lm.cap, mul = CAP ? a.lm.mul / cap : a.lm.mul;
     // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
     auto map = [&](float u) { return CAP ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
@@ -632,6 +633,8 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                     if (buf == 0) tphase ^= 1;
                 }
             } else {
+                // the row's target, or its place in dh: read before the product is waited for
+                const int place = m < live ? (MODE == LOGITS ? a.targets : a.map)[a.row0 + m] : 0;
                 float x[kCols];
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) x[j] = 0.f;
@@ -656,12 +659,12 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
                 if (!ok) break;
                 if (MODE == LOGITS) {
-                    if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, t.nt, part);
+                    if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, place, t.nt, part);
                     __syncwarp();
                 } else {
                     const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
                     if (m < live && n > 0) {
-                        const int64_t o = t.part < 0 ? int64_t(a.map[a.row0 + m]) * a.D + n0
+                        const int64_t o = t.part < 0 ? int64_t(place) * a.D + n0
                                                      : (int64_t(t.part * kPairs + which) * kTile + (m - t.mu * kTile)) * kTile +
                                                            part * kCols;
                         if (t.part < 0 && a.out_bf16) write_row<true>(x, n, static_cast<uint16_t*>(a.out) + o);
