@@ -504,15 +504,16 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             uint32_t phase = 0, tphase = 0;
             bool ok = true;
             for (int i = unit; i < total && ok; i += units) {
-                const LossTile t = tile(i);
-                for (int k = t.k0; k < t.k1 && ok; k += segment) {
+                int k0, k1;
+                loss_steps(i, work, k_total, &k0, &k1);
+                for (int k = k0; k < k1 && ok; k += segment) {
                     if (!tc::mbar_wait_cluster(&tempty[buf], tphase ^ 1, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
                     const uint32_t d = tmem_base + uint32_t(buf * kTile);
-                    const int end = min(k + segment, t.k1);
+                    const int end = min(k + segment, k1);
                     for (int kk = k; kk < end; ++kk) {
                         if (!tc::mbar_wait(&full[stage], phase, abort_flag)) {
                             ok = false;

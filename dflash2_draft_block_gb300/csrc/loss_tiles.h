@@ -28,6 +28,14 @@ struct LossSplit {
     __host__ __device__ int items() const { return whole + rest * ways; }
 };
 
+// The K steps of item i of them: all that the issuer of the products has to know of it.
+__host__ __device__ inline void loss_steps(int i, const LossSplit& work, int k_total, int* k0, int* k1) {
+    const bool split = work.ways > 1 && i >= work.whole;
+    const int kind = split ? (i - work.whole) / work.rest : 0;
+    *k0 = split ? int(int64_t(k_total) * kind / work.ways) : 0;
+    *k1 = split ? int(int64_t(k_total) * (kind + 1) / work.ways) : k_total;
+}
+
 // Item i of them, for pair `which` of the cluster.  LOGITS (h W^T): M fastest in groups, so that W
 // streams past while a group's rows of h stay in L2; quads take two M units.  The gradients: N
 // fastest, so that the clusters of a moment share g's rows; quads take two N tiles.
@@ -64,8 +72,7 @@ __host__ __device__ inline LossTile loss_tile(int i, int n_mu, int n_nt, const L
             t.alone = true;
         }
     }
-    t.k0 = split ? int(int64_t(k_total) * kind / work.ways) : 0;
-    t.k1 = split ? int(int64_t(k_total) * (kind + 1) / work.ways) : k_total;
+    loss_steps(i, work, k_total, &t.k0, &t.k1);
     return t;
 }
 
