@@ -438,9 +438,11 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegisters));
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------------ TMA producer
-            const uint64_t keep = tc::l2_policy_evict_last(), pass = tc::l2_policy_evict_first();
-            const uint64_t pol_a = MODE == LOGITS ? keep : tc::l2_policy_evict_normal();
-            const uint64_t pol_b = MODE == LOGITS ? pass : MODE == DW ? keep : tc::l2_policy_evict_normal();
+            // h stays in L2; W leaves it first where it is read once (one M unit: 2%), and as it comes
+            // where other clusters read it, too (first: it was read twice, 2%)
+            const uint64_t keep = tc::l2_policy_evict_last(), normal = tc::l2_policy_evict_normal();
+            const uint64_t weights = n_mu == 1 ? tc::l2_policy_evict_first() : normal;
+            const uint64_t pol_a = MODE == LOGITS ? keep : normal, pol_b = MODE == DW ? keep : weights;
             int stage = 0;
             uint32_t phase = 0;
             int8_t armed[kStages];
