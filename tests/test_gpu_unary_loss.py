@@ -233,6 +233,62 @@ def test_more_than_one_piece(df2):
         torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("P, V, D", [(1600, 900, 2568), (2100, 600, 136)])
+def test_many_tiles_and_long_sums(df2, P, V, D, dtype):
+    """dh of more tiles than clusters, some whole and some cut, an odd number of them each way; dW's
+    sums of over 2,048 rows, stored and added."""
+    h, W, t, w = inputs(21, P, V, D, masked=0.02)
+    compare(df2, h, W, t, w, dtype=dtype)
+    dW = (torch.randn(V, D, generator=torch.Generator().manual_seed(2)) * 1e-2).to(dtype).cuda()
+    compare(df2, h, W, t, w, dtype=dtype, dW=dW, accumulate=True)
+
+
+def test_loss_alone_in_pieces(df2):
+    """2^24 columns: the statistics of 700 rows go in two pieces; each row is as it is by itself, and
+    some are as the definition says."""
+    V, D, P = 1 << 24, 8, 700
+    h, W, t, w = inputs(22, P, V, D, masked=0.1)
+    loss, lse = df2.unary_ce(h, W, t)
+    for some in (slice(0, 300), slice(300, 555), slice(555, 700)):
+        a, b = df2.unary_ce(h[some], W, t[some])
+        assert torch.equal(a.nan_to_num(-1.0), loss[some].nan_to_num(-1.0))
+        assert torch.equal(b.nan_to_num(-1.0), lse[some].nan_to_num(-1.0))
+    rows = torch.tensor([0, 255, 511, 512, 699], device="cuda")
+    x = h[rows].double() @ W.double().T
+    want = torch.logsumexp(x, 1)
+    live = t[rows] >= 0
+    # five steps of at most 2^-23 of the sum of a logit's terms, exponents, and sums of 2^18 values
+    room = 5 * 2.0 ** -23 * float((h[rows].double().abs().sum(1) * W.double().abs().max()).max()) + 2.0 ** -16
+    assert bool(((lse[rows] - want).abs()[live] <= room).all())
+    assert bool(((loss[rows] - (want - x.gather(1, t[rows].clamp(min=0).long()[:, None])[:, 0])).abs()[live] <= 2 * room).all())
+
+
+def test_two_host_threads(df2):
+    """Calls from two threads on streams of their own, their shapes taking other kernels."""
+    import threading
+    a, b = inputs(34, 700, 3000, 512), inputs(35, 60, 5000, 1032)
+    want = [df2.unary_loss_grad(*s[:3], row_weights=s[3], dW=True, final_logit_softcapping=c) for s, c in ((a, 0.0), (b, 20.0))]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(s, cap, expected):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = df2.unary_loss_grad(*s[:3], row_weights=s[3], dW=True, final_logit_softcapping=cap)
+                stream.synchronize()
+                wrong.extend(not torch.equal(x.nan_to_num(-1.0), y.nan_to_num(-1.0)) for x, y in zip(got, expected))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(s, c, e)) for s, c, e in ((a, 0.0, want[0]), (b, 20.0, want[1]))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert len(wrong) == 160 and not any(wrong)
+
+
 def test_offsets_past_32_bits(df2):
     """A head of 2.46e9 elements: logits, dh and the ends of dW, in fp32 and added in bf16, against sums in
     64 bits a piece of the head at a time."""
