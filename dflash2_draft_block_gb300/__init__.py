@@ -742,12 +742,12 @@ def _loss_inputs(h, W_lm, targets):
     _need(h, "h", torch.bfloat16, 2)
     _need(W_lm, "W_lm", torch.bfloat16, 2)
     _need(targets, "targets", torch.int32)
-    P, D = h.shape
-    if W_lm.shape[1] != D:
+    (P, D), (V, width) = h.shape, W_lm.shape
+    if width != D:
         raise ValueError("W_lm must be [V, D]")
     if targets.numel() != P:
         raise ValueError(f"targets must be [P] ({P}), got {list(targets.shape)}")
-    return P, D, W_lm.shape[0], _device(h, W_lm=W_lm, targets=targets)
+    return P, D, V, _device(h, W_lm=W_lm, targets=targets)
 
 
 def _loss_outputs(out, P, dev, stream):

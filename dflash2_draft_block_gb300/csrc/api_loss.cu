@@ -8,11 +8,11 @@
 namespace {
 
 // Positions a call: the blocks that put the rows with a target in order each count the ones
-// before them, which is P^2 / 256 or so of reading (2 ms at 2^20).
+// before them: P^2 / 512 reads (8 GB of L2, some ms, at 2^20).
 constexpr int64_t kMaxRows = int64_t(1) << 20;
 constexpr int64_t kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kMaxHidden = int64_t(1) << 20;
-// what a piece of rows may take: exponentials in bf16 (the gradients), or statistics (the loss
+// what a piece of rows may take: factors of 16 bits (the gradients), or statistics (the loss
 // alone).  Larger pieces read W fewer times; at 151,936 columns this is 14,080 rows.
 constexpr int64_t kPieceBytes = int64_t(4) << 30;
 constexpr int64_t kPieceStats = int64_t(1) << 30;
