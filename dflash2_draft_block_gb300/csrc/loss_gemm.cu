@@ -13,9 +13,9 @@
 // Sums in pieces.  The tensor core cuts each partial sum off below its last bit instead of
 // rounding it, so a sum of n steps drifts towards zero by about n / 4 ulp: a logit of 4096
 // products came out 4e-6 of itself too small, which a loss would show.  The MMAs
-// therefore sum kSegment K elements at a time into one of two TMEM accumulators while the
-// epilogue warps add the other to running sums in fp32 registers (64 columns a thread, sixteen
-// warps), rounded to nearest.  dW's sums, of the rows of a piece and factors of 8 bits, stay one.
+// therefore sum 1024 K elements at a time (dh, whose factors have 8 bits: 4096) into one of two
+// TMEM accumulators while the epilogue warps add the other to running sums in fp32 registers (64
+// columns a thread, sixteen warps), rounded to nearest.  dW's sums, of a piece's rows, stay one.
 //
 // Roles (640 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-19
 // are the epilogue (TMEM lane = row; four warps a quarter, 64 columns each).  Tiles are
@@ -42,7 +42,8 @@ constexpr int kCols = kLossStats;              // columns of an epilogue thread
 constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
-constexpr int kSegment = 16;                   // stages to a partial sum (1024 K elements)
+constexpr int kSegment = 16;                   // stages to a partial sum of the logits (1024 K elements)
+constexpr int kLongSegment = 64;               // of dh (1%: 16)
 constexpr int kStagedSteps = 32;               // dW's sums of up to 64 times this many rows go out staged
 constexpr uint32_t kStaging = 4096;            // bytes of an epilogue warp: 128 of each of its 32 rows
 __host__ __device__ constexpr int stages(bool staged) { return staged ? 5 : 7; }
@@ -433,7 +434,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
     auto tile = [&](int i) { return loss_tile<MODE == LOGITS, QUAD>(i, n_mu, n_nt, work, k_total, which); };
 
-    const int segment = MODE == DW ? max(k_total, 1) : kSegment;
+    const int segment = MODE == DW ? max(k_total, 1) : MODE == DH ? kLongSegment : kSegment;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegisters));
         if (warp == 0 && lane == 0) {
