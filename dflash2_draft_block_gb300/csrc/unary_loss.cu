@@ -7,9 +7,14 @@
 // so a row that is all but certain keeps its small loss and gradient to fp32's precision.
 //
 //   live_rows_kernel   the rows that have a target, in order, copied next to each other: the
-//                      products neither compute the others nor meet a NaN in them
-//   row_loss_kernel    a row's loss from its tiles' statistics, and its e to g in place
-//   sum_parts_kernel   the rows of dh whose sums were cut, from their parts in order
+//                      products neither compute the others nor meet a NaN in them.  Bound by
+//                      the copy (4096 rows of 4096: 18 us; 16,384: 46 us, 5.8 TB/s), or for few rows by
+//                      two dependent loads (4 us)
+//   row_loss_kernel    a row's loss from its tiles' statistics, and its e to g in place.  Bound
+//                      by HBM: 4096 rows of 151,936 in 390 us, 6.4 TB/s with four loads a thread in flight
+//                      (415 with one)
+//   sum_parts_kernel   the rows of dh whose sums were cut, from their parts in order (13 us for
+//                      20 tiles in 9 to 13 parts)
 #include <cuda_fp16.h>
 
 #include "common.cuh"
