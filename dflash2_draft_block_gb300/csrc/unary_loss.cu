@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
             const int64_t at = c + k * kThreads * 8;
             if (at < c1) {
                 in[k] = __ldcs(reinterpret_cast<const uint4*>(e + at));
-                m[k] = __ldg(&stats[at / kLossStats].x);
+                m[k] = stats[at / kLossStats].x;  // written while this kernel may have begun: no read-only load
             }
         }
 #pragma unroll
