@@ -160,8 +160,17 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     const float cap = a.lm.cap, mul = CAP ? a.lm.mul / cap : a.lm.mul;
     // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
     auto map = [&](float u) { return CAP ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
-    if ((t >= 0 && t < kCols) || c0 + kCols > a.V) {  // the target and what is no column are left out
-        const int end = c0 + kCols > a.V ? int(a.V - c0) : kCols;
+    // The columns left out, the target and what is no column: as bits, and in x below any logit.  (Not
+    // by that value afterwards: a logit may be -infinity itself, which a cap makes -cap.)
+    uint32_t out_lo = 0u, out_hi = 0u;
+    if ((t >= 0 && t < kCols) || c0 + kCols > a.V) {
+        const int end = c0 >= a.V ? 0 : c0 + kCols > a.V ? int(a.V - c0) : kCols;
+        if (CAP) {
+            uint64_t out = end < kCols ? ~uint64_t(0) << end : 0u;
+            if (t >= 0 && t < kCols) out |= uint64_t(1) << t;
+            out_lo = uint32_t(out);
+            out_hi = uint32_t(out >> 32);
+        }
         float xt = 0.f;
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 32) {
@@ -177,7 +186,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     float top = -INFINITY;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) top = fmaxf(top, x[j]);
-    const bool none = top == -INFINITY;
+    const bool none = CAP ? (out_lo & out_hi) == 0xFFFFFFFFu : top == -INFINITY;
     // x - M in the units of the logits as they are mapped: without a cap the multiplier waits
     const float base = none ? 0.f : CAP ? map(top) : top;
     const float by = CAP ? kLog2e : __fmul_rn(kLog2e, mul);
@@ -185,6 +194,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
     auto columns = [&](int at, int c) {  // x[at .. at + 32), the row's columns from c on
+        const uint32_t left_out = c == 0 ? out_lo : out_hi;
 #pragma unroll
         for (int j0 = 0; j0 < 32; j0 += 16) {
             uint32_t word[8];
@@ -195,7 +205,7 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
                 for (int k = 0; k < 2; ++k) {
                     const float u = x[at + j0 + j + k], v = CAP ? map(u) : u;
                     e[k] = exp2_fast(__fmul_rn(__fsub_rn(v, base), by));
-                    if (CAP && u == -INFINITY) e[k] = 0.f;
+                    if (CAP && (left_out >> (j0 + j + k) & 1u)) e[k] = 0.f;
                     sum[(j + k) & 3] = __fadd_rn(sum[(j + k) & 3], e[k]);
                     const float bent = v * inv_cap;
                     e[k] *= CAP ? fmaf(-kExpScale * bent, bent, kExpScale) : kExpScale;

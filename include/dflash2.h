@@ -482,7 +482,8 @@ int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int6
  * are fp32, and the loss of a row that is all but certain of its target does not cancel.
  * A row without a target (targets[p] < 0) gives NaN in both and is not computed (its h may
  * hold anything); a target >= V does the same and sets DF2_STATUS_ID_OUT_OF_RANGE.  A NaN in
- * another row's h reaches that row's loss, and no other.
+ * another row's h reaches that row's loss, and no other.  An infinite logit is c or -c under a
+ * softcap; without one -infinity has no share in the sum, and +infinity gives NaN.
  *
  *   h [P, D] bf16; W_lm [V, D] bf16; targets [P] int32
  *   loss [P] fp32 out; lse [P] fp32 out, nullable
