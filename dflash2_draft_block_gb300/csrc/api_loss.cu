@@ -39,7 +39,7 @@ struct Plan {
     int64_t pieces;
     int64_t e_rows, e_ld;
     int n_stats;
-    size_t count, map, targets, target_logit, h, stats, e, part, sums, bytes;
+    size_t count, map, targets, target_logit, target_slope, h, stats, e, part, sums, bytes;
 };
 
 Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
@@ -65,6 +65,7 @@ Plan make_plan(int64_t P, int64_t D, int64_t V, bool dh, bool dw, int num_sms) {
     p.map = take(size_t(P) * 4);
     p.targets = take(size_t(P) * 4);
     p.target_logit = take(size_t(P) * 4);
+    p.target_slope = take(grads ? size_t(P) * 4 : 0);
     p.h = take(size_t(p.h_rows) * D * 2);
     p.stats = take(size_t(p.rows) * p.n_stats * 8);
     p.e = take(grads ? size_t(p.e_rows) * p.e_ld * 2 : 0);
@@ -140,6 +141,7 @@ cudaError_t run(const Call& c, const Plan& p, int num_sms) {
         g.status = c.status;
         g.targets = rows.live_targets;
         g.target_logit = reinterpret_cast<float*>(c.ws + p.target_logit);
+        g.target_slope = reinterpret_cast<float*>(c.ws + p.target_slope);
         g.stats = reinterpret_cast<float2*>(c.ws + p.stats);
         g.n_stats = p.n_stats;
         g.lm = c.lm;
@@ -147,7 +149,7 @@ cudaError_t run(const Call& c, const Plan& p, int num_sms) {
         g.e_ld = p.e_ld;
         e = df2::loss_logits_launch(g, rows.live_h, p.h_rows, c.W, num_sms, c.stream);
         if (e != cudaSuccess) break;
-        const df2::LossRowArgs r{g.count, g.row0, g.rows, c.V, g.stats, g.n_stats, g.target_logit, g.targets, g.map,
+        const df2::LossRowArgs r{g.count, g.row0, g.rows, c.V, g.stats, g.n_stats, g.target_logit, g.target_slope, g.targets, g.map,
                                  c.weights, c.lm, c.loss, c.lse, g.e, g.e_ld};
         e = df2::loss_row_launch(r, p.e_rows, num_sms, c.stream);
         if (e != cudaSuccess) break;

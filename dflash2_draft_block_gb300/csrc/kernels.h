@@ -177,6 +177,7 @@ struct LossGemmArgs {
     // logits
     const int32_t* targets;   // live_targets
     float* target_logit;      // [P], of the live rows
+    float* target_slope;      // [P]: the softcap's slope at the target's logit, over lm.mul (with e and a cap)
     float2* stats;            // [rows, n_stats]: (M, sum of exp(x - M)) of kLossStats columns each
     int n_stats;
     LogitMap lm;
@@ -225,6 +226,7 @@ struct LossRowArgs {
     const float2* stats;
     int n_stats;
     const float* target_logit;
+    const float* target_slope;  // read with e and a cap
     const int32_t* live_targets;
     const int32_t* map;
     const float* weights;     // [P], nullable

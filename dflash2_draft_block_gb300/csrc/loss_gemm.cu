@@ -122,12 +122,24 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// cap * tanh(y), to about 2^-21 of it: tanh y = 1 - 2 / (exp(2 y) + 1), and where that would
-// cancel the series y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835.
-__device__ __forceinline__ float bend(float y, float cap) {
+// r = 1 / (exp(2 |y|) + 1), of which both tanh and its slope are made: |tanh y| = 1 - 2 r, and
+// 1 - tanh^2 y = 4 r (1 - r), which keeps its bits where tanh is all but 1 (1 - tanh^2 itself is off
+// by 3% at y = 7, and by 20% at 8).
+__device__ __forceinline__ float tanh_gap(float y) {
     float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(y * (2.f * kLog2e)) + 1.f));
-    const float wide = fmaf(-2.f, r, 1.f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(exp2_fast(fabsf(y) * (2.f * kLog2e)) + 1.f));
+    return r;
+}
+// `scale` times the slope.
+__device__ __forceinline__ float tanh_slope(float r, float scale) {
+    const float s = 4.f * scale * r;
+    return fmaf(-s, r, s);
+}
+
+// cap * tanh(y), to about 2^-21 of it: 1 - 2 r, and where that would cancel the series
+// y - y^3/3 + 2 y^5/15 - 17 y^7/315 + 62 y^9/2835.
+__device__ __forceinline__ float bend(float y, float r, float cap) {
+    const float wide = copysignf(fmaf(-2.f, r, 1.f), y);
     const float q = y * y;
     float s = fmaf(q, 0.021869488536155203f, -0.053968253968253970f);
     s = fmaf(q, s, 0.13333333333333333f);
@@ -149,9 +161,9 @@ __device__ __forceinline__ void store8(void* p, const uint32_t (&w)[8], bool wid
     }
 }
 
-// One row's 64 logits of a tile (x, raw): the statistics, and e where asked, in fp16 in
-// units of 2^-15 (11 bits of exp(x - M) down to M - 20, then fewer until M - 27; bf16 here and
-// again as g would double the factors' rounding error).
+// One row's 64 logits of a tile (x, raw): the statistics, and e where asked, with a cap times its
+// slope, in fp16 in units of 2^-15 (11 bits down to 2^-29, that is exp(x - M) at M - 20, then fewer
+// until 2^-40; bf16 here and again as g would double the factors' rounding error).
 template <bool E, bool CAP>
 __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x)[kCols], int row, int target, int nt,
                                                 int part) {
@@ -159,7 +171,10 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     const int64_t t = target - c0;
     const float cap = a.lm.cap, mul = CAP ? a.lm.mul / cap : a.lm.mul;
     // Non-decreasing.  Rounded as written, so that the loss is the same with e and without.
-    auto map = [&](float u) { return CAP ? bend(__fmul_rn(u, mul), cap) : __fmul_rn(u, mul); };
+    auto map = [&](float u) {
+        const float y = __fmul_rn(u, mul);
+        return CAP ? bend(y, tanh_gap(y), cap) : y;
+    };
     // The columns left out, the target and what is no column: as bits, and in x below any logit.  (Not
     // by that value afterwards: a logit may be -infinity itself, which a cap makes -cap.)
     uint32_t out_lo = 0u, out_hi = 0u;
@@ -181,7 +196,10 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
             }
             turn(x);
         }
-        if (t >= 0 && t < kCols) a.target_logit[a.row0 + row] = map(xt);
+        if (t >= 0 && t < kCols) {
+            a.target_logit[a.row0 + row] = map(xt);
+            if (E && CAP) a.target_slope[a.row0 + row] = tanh_slope(tanh_gap(__fmul_rn(xt, mul)), 1.f);
+        }
     }
     float top = -INFINITY;
 #pragma unroll
@@ -190,7 +208,6 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
     // x - M in the units of the logits as they are mapped: without a cap the multiplier waits
     const float base = none ? 0.f : CAP ? map(top) : top;
     const float by = CAP ? kLog2e : __fmul_rn(kLog2e, mul);
-    const float inv_cap = CAP ? 1.f / cap : 0.f;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     uint16_t* out = E ? a.e + int64_t(row) * a.e_ld + c0 : nullptr;
     auto columns = [&](int at, int c) {  // x[at .. at + 32), the row's columns from c on
@@ -203,12 +220,12 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
                 float e[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float u = x[at + j0 + j + k], v = CAP ? map(u) : u;
+                    const float u = x[at + j0 + j + k], y = __fmul_rn(u, mul), r = CAP ? tanh_gap(y) : 0.f;
+                    const float v = CAP ? bend(y, r, cap) : u;
                     e[k] = exp2_fast(__fmul_rn(__fsub_rn(v, base), by));
                     if (CAP && (left_out >> (j0 + j + k) & 1u)) e[k] = 0.f;
                     sum[(j + k) & 3] = __fadd_rn(sum[(j + k) & 3], e[k]);
-                    const float bent = v * inv_cap;
-                    e[k] *= CAP ? fmaf(-kExpScale * bent, bent, kExpScale) : kExpScale;
+                    e[k] *= CAP ? tanh_slope(r, kExpScale) : kExpScale;
                 }
                 if (E) word[j / 2] = pack_f16(e[0], e[1]);
             }

@@ -143,8 +143,7 @@ __global__ void __launch_bounds__(kThreads) row_loss_kernel(const LossRowArgs a)
     if (!G) return;
     const float w = (a.weights ? a.weights[p] : 1.f) * a.lm.mul / all;
     const float w_e = w / kExpScale;
-    const float bent = a.lm.cap > 0.f ? xt / a.lm.cap : 0.f;
-    const float gt = -sum * w * (1.f - bent * bent);
+    const float gt = -sum * w * (a.lm.cap > 0.f ? a.target_slope[a.row0 + row] : 1.f);
     const int64_t t = a.live_targets[a.row0 + row];
     uint16_t* e = a.e + row * a.e_ld;
     constexpr int kAhead = 4;  // units of a thread that are loaded together

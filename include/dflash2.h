@@ -508,8 +508,9 @@ int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_
  * loss is not weighted; the gradients are those of sum_p w_p * loss_p.  A row without a target
  * contributes nothing: dh zero, its h and weight not used.
  * The factors g are rounded to bf16 for the products (2^-8 of each), whatever the gradients'
- * type, from exp(U' - M) held in fp16, M the largest of 64 columns (2^-11 of each, and 2^-40
- * of the largest).  Sums are fp32 in an
+ * type, from exp(U' - M) f'(U) / m held in fp16, M the largest of 64 columns (2^-11 of each,
+ * and 2^-40 of exp(M - lse) m w, which is felt where a cap is so far saturated that its slope
+ * is below 2^-29).  The slope keeps fp32's bits however far that is.  Sums are fp32 in an
  * order the shapes and the rows with a target fix, so equal inputs give equal bits; dh and dW
  * are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it
  * is written.
