@@ -13,9 +13,11 @@
 // Sums in pieces.  The tensor core cuts each partial sum off below its last bit instead of
 // rounding it, so a sum of n steps drifts towards zero by about n / 4 ulp: a logit of 4096
 // products came out 4e-6 of itself too small, which a loss would show.  The MMAs
-// therefore sum 1024 K elements at a time (dh, whose factors have 8 bits: 4096) into one of two
-// TMEM accumulators while the epilogue warps add the other to running sums in fp32 registers (64
-// columns a thread, sixteen warps), rounded to nearest.  dW's sums, of a piece's rows, stay one.
+// therefore sum 1024 K elements at a time (dh and dW, whose factors have 8 bits: 4096) into one of
+// two TMEM accumulators while the epilogue warps add the other to running sums in fp32 registers (64
+// columns a thread, sixteen warps), rounded to nearest.  dW of up to 4096 rows is one such sum and
+// goes out as it lies in TMEM; of more rows it is added up like the others (DW_LONG: one sum of 2^20
+// rows came out 6e-3 too small).
 //
 // Roles (640 threads): warp 0 lane 0 issues the TMA loads, warp 1 lane 0 the MMAs, warps 4-19
 // are the epilogue (TMEM lane = row; four warps a quarter, 64 columns each).  Tiles are
@@ -47,7 +49,7 @@ constexpr int kTile = 256;
 constexpr int kStep = 64;                      // K elements a stage
 constexpr uint32_t kOperand = 128 * kStep * 2;  // bytes a stage and CTA of one operand
 constexpr int kSegment = 16;                   // stages to a partial sum of the logits (1024 K elements)
-constexpr int kLongSegment = 64;               // of dh (1%: 16)
+constexpr int kLongSegment = 64;               // of dh (1%: 16) and of dW
 constexpr int kStagedSteps = 32;               // dW's sums of up to 64 times this many rows go out staged
 constexpr uint32_t kStaging = 4096;            // bytes of an epilogue warp: 128 of each of its 32 rows
 __host__ __device__ constexpr int stages(bool staged) { return staged ? 5 : 7; }
@@ -55,7 +57,7 @@ __host__ __device__ constexpr uint32_t smem_bytes(bool staged) {
     return stages(staged) * 2 * kOperand + (staged ? 16 * kStaging : 0) + (2 * stages(staged) + 5 + 16) * 8 + 16 + 1024;
 }
 
-enum { LOGITS, DH, DW };
+enum { LOGITS, DH, DW, DW_LONG };
 
 struct Work {
     LossGemmArgs a;
@@ -246,8 +248,9 @@ __device__ __forceinline__ void logits_epilogue(const LossGemmArgs& a, float (&x
         make_float2(none ? top : CAP ? base : __fmul_rn(top, mul), (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
-// x += the columns [0, n) (n a multiple of 8) at p: their loads are waited for once.
-__device__ __forceinline__ void add_row(float (&x)[32], int n, const float* p) {
+// The first 32 of x += the columns [0, n) (n a multiple of 8) at p: their loads are waited for once.
+template <int N>
+__device__ __forceinline__ void add_row(float (&x)[N], int n, const float* p) {
     float4 f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -258,6 +261,20 @@ __device__ __forceinline__ void add_row(float (&x)[32], int n, const float* p) {
         x[4 * j + 1] += f[j].y;
         x[4 * j + 2] += f[j].z;
         x[4 * j + 3] += f[j].w;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void add_row(float (&x)[N], int n, const uint16_t* p) {
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = 8 * j < n ? reinterpret_cast<const uint4*>(p)[j] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float f[8];
+        unpack8(w[j], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[8 * j + k] += f[k];
     }
 }
 
@@ -401,7 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                  const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Work w) {
     constexpr int kStages = stages(STAGED);
-    constexpr bool A_MN = MODE == DW, B_MN = MODE != LOGITS;
+    constexpr bool DW_ANY = MODE == DW || MODE == DW_LONG;
+    constexpr bool A_MN = DW_ANY, B_MN = MODE != LOGITS;
     const LossGemmArgs& a = w.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -455,7 +473,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
     // the rows of this piece that have a target
     const int64_t left = int64_t(*a.count) - a.row0;
     const int live = left < 0 ? 0 : left > a.rows ? a.rows : int(left);
-    const int n_mu = (int(MODE == DW ? a.V : live) + kTile - 1) / kTile;
+    const int n_mu = (int(DW_ANY ? a.V : live) + kTile - 1) / kTile;
     const int k_total = (int(MODE == LOGITS ? a.D : MODE == DH ? a.V : live) + kStep - 1) / kStep;
     const int units = int(gridDim.x) / (2 * kPairs), unit = int(blockIdx.x) / (2 * kPairs);
     const int n_nt = w.n_nt;
@@ -465,7 +483,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
 
     auto tile = [&](int i) { return loss_tile<MODE == LOGITS, QUAD>(i, n_mu, n_nt, work, k_total, which); };
 
-    const int segment = MODE == DW ? max(k_total, 1) : MODE == DH ? kLongSegment : kSegment;
+    const int segment = MODE == DW ? max(k_total, 1) : MODE == LOGITS ? kSegment : kLongSegment;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRoleRegisters));
         if (warp == 0 && lane == 0) {
@@ -474,7 +492,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
             // where other clusters read it, too (first: it was read twice, 2%)
             const uint64_t keep = tc::l2_policy_evict_last(), normal = tc::l2_policy_evict_normal();
             const uint64_t weights = n_mu == 1 ? tc::l2_policy_evict_first() : normal;
-            const uint64_t pol_a = MODE == LOGITS ? keep : normal, pol_b = MODE == DW ? keep : weights;
+            const uint64_t pol_a = MODE == LOGITS ? keep : normal, pol_b = DW_ANY ? keep : weights;
             int stage = 0;
             uint32_t phase = 0;
             int8_t armed[kStages];
@@ -511,7 +529,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                         } else {
                             shared(da, &tm_a, k * kStep, ma, pol_a);
                         }
-                        const int kb = k * kStep + (MODE == DW ? int(a.row0) : 0);
+                        const int kb = k * kStep + (DW_ANY ? int(a.row0) : 0);
                         own(db, &tm_b, nb, kb, pol_b);
                         own(db + kOperand / 2, &tm_b, nb + 64, kb, pol_b);
                     }
@@ -669,7 +687,7 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 }
             } else {
                 // the row's target, or its place in dh: read before the product is waited for
-                const int place = m < live ? (MODE == LOGITS ? a.targets : a.map)[a.row0 + m] : 0;
+                const int place = !DW_ANY && m < live ? (MODE == LOGITS ? a.targets : a.map)[a.row0 + m] : 0;
                 float x[kCols];
 #pragma unroll
                 for (int j = 0; j < kCols; ++j) x[j] = 0.f;
@@ -695,6 +713,27 @@ loss_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant
                 if (!ok) break;
                 if (MODE == LOGITS) {
                     if (m < live && t.nt < n_nt) logits_epilogue<E, CAP>(a, x, m, place, t.nt, part);
+                    __syncwarp();
+                } else if (MODE == DW_LONG) {
+                    const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
+#pragma unroll 1
+                    for (int c = 0; c < kCols; c += 32) {
+                        const int64_t o = int64_t(m) * a.D + n0 + c;
+                        if (m < a.V && c < n) {
+                            if (a.sums && !a.first) add_row(x, n - c, a.sums + o);
+                            void* to = a.sums + o;
+                            if (a.last) to = static_cast<char*>(a.out) + o * (a.out_bf16 ? 2 : 4);
+                            const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;
+                            if (a.last && a.out_bf16) {
+                                if (a.accumulate) add_row(x, n - c, static_cast<const uint16_t*>(to));
+                                write32<true>(x, n - c, to, wide);
+                            } else {
+                                if (a.last && a.accumulate) add_row(x, n - c, static_cast<const float*>(to));
+                                write32<false>(x, n - c, to, wide);
+                            }
+                        }
+                        turn(x);
+                    }
                     __syncwarp();
                 } else {
                     const int n0 = t.nt * kTile + part * kCols, n = min(kCols, int(a.D) - n0);
@@ -868,6 +907,7 @@ cudaError_t loss_dw_launch(const LossGemmArgs& a, int64_t e_rows, const uint16_t
         if (!make_map(&to, a.out, a.V, a.D, a.D, 32, !a.out_bf16)) return cudaErrorInvalidValue;
         return launch<DW, false, false, true>(ta, tb, to, w, across, w.n_nt, num_sms, stream);
     }
+    if (up(a.rows, kStep) > kLongSegment) return launch<DW_LONG>(ta, tb, tb, w, across, w.n_nt, num_sms, stream);
     return launch<DW>(ta, tb, tb, w, across, w.n_nt, num_sms, stream);
 }
 

@@ -510,9 +510,11 @@ int dflash2_unary_ce(const uint16_t* h, int64_t P, int64_t D, const uint16_t* W_
  * The factors g are rounded to bf16 for the products (2^-8 of each), whatever the gradients'
  * type, from exp(U' - M) f'(U) / m held in fp16, M the largest of 64 columns (2^-11 of each,
  * and 2^-40 of exp(M - lse) m w, which is felt where a cap is so far saturated that its slope
- * is below 2^-29).  The slope keeps fp32's bits however far that is.  Sums are fp32 in an
- * order the shapes and the rows with a target fix, so equal inputs give equal bits; dh and dW
- * are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it
+ * is below 2^-29).  The slope keeps fp32's bits however far that is.  Sums are fp32: the
+ * tensor core's, which cut below their last bit, of at most 1,024 products for a logit and of 4,096
+ * for dh (columns) and dW (rows), off by 2^-15 of the terms' sizes at most, and those rounded to
+ * nearest.  Their order is fixed by the shapes and the rows with a target, so equal inputs give
+ * equal bits; dh and dW are rounded to their type once.  accumulate adds to dW as it is, otherwise every row of it
  * is written.
  * Rows go in pieces of at most 4 GiB of such factors (or 256 rows' where those are more): the
  * workspace does not grow with P beyond that but for a copy of h, and with dW the fp32 sums of
