@@ -180,7 +180,9 @@ int call(Call c, float multiplier, float cap, void* workspace, size_t workspace_
     const int rc = check_shape(c.P, c.D, c.V);
     if (rc != DF2_OK) return rc;
     if (!(multiplier > 0.f) || !(multiplier <= FLT_MAX) || !(cap >= 0.f) || !(cap <= FLT_MAX)) return DF2_ERR_INVALID_ARGUMENT;
-    if (cap > 0.f && !(1.f / cap <= FLT_MAX && multiplier / cap <= FLT_MAX)) return DF2_ERR_UNSUPPORTED;
+    // m / c is a factor of its own: neither infinite nor short of bits
+    if (cap > 0.f && !(1.f / cap <= FLT_MAX && multiplier / cap <= FLT_MAX && multiplier / cap >= FLT_MIN))
+        return DF2_ERR_UNSUPPORTED;
     // exp's argument is taken from the raw difference times log2(e) m (loss_gemm.cu)
     if (cap == 0.f && !(1.4426950408889634f * multiplier <= FLT_MAX)) return DF2_ERR_UNSUPPORTED;
     c.lm.mul = multiplier;

@@ -491,8 +491,9 @@ int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targets, int6
  *             statistics of 64 columns each (more rows go in pieces), or 256 rows' where those
  *             are more
  * Rules: P >= 0, V >= 1, D >= 1, D % 8 == 0; output_multiplier m and final_logit_softcapping c as
- * dflash2_unary_topk; P <= 2^20, V <= 2^24, D <= 2^20; in fp32 1 / c and m / c finite, or with
- * c = 0 log2(e) m (else DF2_ERR_UNSUPPORTED); outputs must not overlap inputs or one another.
+ * dflash2_unary_topk; P <= 2^20, V <= 2^24, D <= 2^20; in fp32 1 / c and m / c finite and m / c
+ * normal, or with c = 0 log2(e) m finite (else DF2_ERR_UNSUPPORTED); outputs must not overlap
+ * inputs or one another.
  * h and W_lm 16-byte aligned, the rest by their elements.
  * ---------------------------------------------------------------------- */
 size_t dflash2_unary_ce_workspace_size(int64_t P, int64_t D, int64_t V);

@@ -35,3 +35,15 @@ def test_multipliers_whose_exponent_overflows(calls):
             assert calls(float(mul), 0.0) in ((NO_DEVICE, NO_WORKSPACE) if fits else (UNSUPPORTED,)), mul
         assert not np.isfinite(log2e * np.float32(2.4e38)) and np.isfinite(log2e * np.float32(2.3e38))
     assert calls(2.4e38, 1e10) in (NO_DEVICE, NO_WORKSPACE)  # (m / c and log2(e) apart)
+
+
+def test_caps_whose_quotient_is_subnormal(calls):
+    """tanh's argument is the logit times m / c: below 2^-126 that has lost bits (1e-5 / 1e38 is off by
+    half a percent, and every logit with it)."""
+    quotient = np.float32(1e-5) / np.float32(1e38)
+    assert abs(float(quotient) / (float(np.float32(1e-5)) / float(np.float32(1e38))) - 1.0) > 1e-3
+    least = np.finfo(np.float32).tiny
+    for mul, cap in ((1e-5, 1e38), (1e-30, 1e30), (1.0, 3e38), (1e-37, 30.0), (1e-38, 0.5)):
+        fits = bool(np.float32(mul) / np.float32(cap) >= least)
+        assert calls(mul, cap) in ((NO_DEVICE, NO_WORKSPACE) if fits else (UNSUPPORTED,)), (mul, cap)
+    assert calls(1.0, 8e37) in (NO_DEVICE, NO_WORKSPACE) and calls(1e-37, 0.0) in (NO_DEVICE, NO_WORKSPACE)
