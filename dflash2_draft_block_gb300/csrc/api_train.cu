@@ -5,6 +5,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "row_spans.h"
 
 namespace {
 
@@ -224,12 +225,9 @@ DF2_API int dflash2_selector_loss_grad(const int32_t* pred, const int32_t* targe
 
 namespace {
 
-// [N, D] elements `ld` apart a row: whether two such tensors share bytes.
-bool overlap(const void* p, int64_t p_ld, int p_dtype, const void* q, int64_t q_ld, int q_dtype, int64_t N, int64_t D) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    const uintptr_t an = uintptr_t((N - 1) * p_ld + D) * (p_dtype == DF2_DTYPE_BF16 ? 2 : 4);
-    const uintptr_t bn = uintptr_t((N - 1) * q_ld + D) * (q_dtype == DF2_DTYPE_BF16 ? 2 : 4);
-    return a < b + bn && b < a + an;
+df2::RowSpan span(const void* p, int dtype, int64_t D, int64_t ld) {
+    const int64_t size = dtype == DF2_DTYPE_BF16 ? 2 : 4;
+    return {reinterpret_cast<uintptr_t>(p), D * size, ld * size};
 }
 
 }  // namespace
@@ -247,10 +245,11 @@ DF2_API int dflash2_dropout(const void* x, int x_dtype, int64_t N, int64_t D, in
         (reinterpret_cast<uintptr_t>(draw_at) & 7u))
         return DF2_ERR_UNSUPPORTED;
     // in place is fine (an element is read before it is written), a shifted overlap is not
-    if (overlap(x, x_ld, x_dtype, out, out_ld, out_dtype, N, D) &&
+    const df2::RowSpan out_span = span(out, out_dtype, D, out_ld);
+    if (df2::rows_share_bytes(span(x, x_dtype, D, x_ld), out_span, N) &&
         !(x == out && x_dtype == out_dtype && (x_ld == out_ld || N == 1)))
         return DF2_ERR_INVALID_ARGUMENT;
-    if (residual && overlap(residual, residual_ld, out_dtype, out, out_ld, out_dtype, N, D) &&
+    if (residual && df2::rows_share_bytes(span(residual, out_dtype, D, residual_ld), out_span, N) &&
         !(residual == out && (residual_ld == out_ld || N == 1)))
         return DF2_ERR_INVALID_ARGUMENT;
     const df2::DropoutArgs a{x, x_dtype == DF2_DTYPE_BF16, x_ld, N, D, uint32_t(std::floor(rate * 65536.0 + 0.5)), seed,

@@ -653,7 +653,9 @@ int dflash2_adamw(const dflash2_adamw_tensor* tensors, int count, int state_bits
  *                      (DF2_ERR_UNSUPPORTED).
  *   residual [N, D] out_dtype, rows residual_ld apart, nullable
  *   out      [N, D] out_dtype, rows out_ld apart.  It may be x (same dtype and rows) or
- *                      residual; any other overlap is DF2_ERR_INVALID_ARGUMENT.
+ *                      residual; any other overlap is DF2_ERR_INVALID_ARGUMENT (rows that are
+ *                      equally far apart may lie between one another, as halves of one wide
+ *                      matrix do).
  * Rules: N >= 0, D >= 1, 0 <= rate <= 1; N * D <= 2^40 (else DF2_ERR_UNSUPPORTED).
  * Tensors need only their elements' alignment; 16-byte aligned ones that are dense, or have
  * D and strides a multiple of 8, run faster.
