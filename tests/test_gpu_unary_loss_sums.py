@@ -61,3 +61,28 @@ def test_rows_without_a_target_change_no_sum(df2, live, dtype):
     b = df2.unary_loss_grad(h[some], W, t[some], dW=True, dtype=dtype)
     assert torch.equal(a[3], b[3])
     assert torch.equal(a[0][some], b[0])
+
+
+def test_replays_with_other_rows(df2):
+    """A captured capped call of many rows, replayed with all of them, some and next to none live: the
+    targets' slopes and the pieces of dW's sums are those of the rows of that replay."""
+    P, V, D = 9000, 500, 72
+    g = torch.Generator().manual_seed(6)
+    h, W = torch.randn(P, D, generator=g).to(BF).cuda(), (torch.randn(V, D, generator=g) / 3).to(BF).cuda()
+    ws = torch.empty(df2.unary_loss_grad_workspace_size(P, D, V, True, True), dtype=torch.uint8, device="cuda")
+    t = torch.randint(0, V, (P,), generator=g).to(I32).cuda()
+    dh, dW = torch.empty(P, D, device="cuda"), torch.empty(V, D, device="cuda")
+    out = (torch.empty(P, device="cuda"), torch.empty(P, device="cuda"))
+    df2.unary_loss_grad(h, W, t, final_logit_softcapping=2.0, dW=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        df2.unary_loss_grad(h, W, t, final_logit_softcapping=2.0, dh=dh, dW=dW, workspace=ws, out=out)
+    every = t.clone()
+    for masked in (0.0, 0.4, 0.6, 0.999, 0.0):
+        t.copy_(torch.where(torch.rand(P, generator=g).cuda() < masked, torch.full_like(every, -1), every.roll(7)))
+        h.copy_(h.roll(1, 0))
+        ws.fill_(0xFF)  # nothing is left over from a replay before
+        graph.replay()
+        want = df2.unary_loss_grad(h, W, t, final_logit_softcapping=2.0, dW=True, dtype=F32)
+        for a, b in zip((*out, dh, dW), want):
+            assert torch.equal(a.nan_to_num(-1.0), b.nan_to_num(-1.0))
